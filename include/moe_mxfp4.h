@@ -396,6 +396,155 @@ typedef struct {
 moe_status moe_layer(const moe_dims* dims, const moe_layer_args* args,
                      void* ws, size_t ws_bytes, void* stream);
 
+/* --- dense operators -----------------------------------------------------------
+ * (No counterpart in the pages: the dense companions of the routed layer, for
+ * serving and training the dense projections and feed-forward blocks that
+ * stand beside it.)
+ *
+ * A projection with a fused epilogue (moe_linear), a gated feed-forward block
+ * (moe_ffn), their backward passes, and activation checkpoints in 8 bits that
+ * the block's forward pass writes and its backward pass reads.
+ *
+ * Conventions, beside those at the top of this file:
+ * - "16-bit" is the type of dims->dtype (bf16 or IEEE f16), for inputs,
+ *   weights, bias, residual and saved activations; all of one call share it.
+ *   Outputs and gradients are 16-bit, or fp32 with out_f32 = 1.
+ * - Products accumulate in fp32; bias, activation, residual and the slopes of
+ *   the backward pass are applied in fp32. Tensors between two products (h,
+ *   dz, dg, du) are rounded once to 16 bits (nearest even), as tensor cores
+ *   take them; everything else is rounded once, when it is stored.
+ * - Sizes: 1 <= T <= 65536; N, K, H, I multiples of 8 in [8, 65536].
+ * - ld* are row pitches in elements, 0 for packed rows; a pitch is a multiple
+ *   of 8, not below the row's length and below 2^31. Elements between a row's
+ *   end and the next row are neither read nor written. Weights, weight
+ *   gradients and saved activations are packed.
+ * - y may be the residual itself (the same pointer and pitch, 16-bit output);
+ *   otherwise outputs overlap no input and no other output.
+ * - Infinities and NaN propagate as IEEE arithmetic has them, within the rows
+ *   and columns that use them.
+ * - Results are the same bits on every call with the same inputs: no sum
+ *   depends on an order that varies.
+ * - The workspace: moe_linear_workspace_size() / moe_ffn_workspace_size()
+ *   bytes, 16-byte aligned, for the forward and the backward call of those
+ *   dims; moe_dense_workspace_init() once before its first use (it clears the
+ *   status word that moe_device_status() reads: only bit 2 can be set here).
+ *   Nothing in it is kept from one call for the next. Calls that share a
+ *   workspace must not overlap in time (captured graphs included).
+ */
+typedef enum {
+  MOE_BF16 = 0,
+  MOE_F16 = 1
+} moe_dtype;
+
+/* Activation functions, with z the fp32 argument. */
+typedef enum {
+  MOE_FN_NONE = 0,   /* z */
+  MOE_FN_SILU = 1,   /* z / (1 + e^-z) */
+  MOE_FN_GELU = 2,   /* z Phi(z), Phi the normal distribution function (erf form) */
+  MOE_FN_RELU = 3    /* max(z, 0); slope 0 at 0 */
+} moe_fn;
+
+/* What the forward pass of the gated block keeps for its backward pass. */
+typedef enum {
+  MOE_SAVE_NONE = 0,  /* nothing (serving) */
+  MOE_SAVE_16 = 1,    /* g and u in 16 bits */
+  MOE_SAVE_8 = 2      /* g, u and optionally x as 8-bit checkpoints */
+} moe_save;
+
+moe_status moe_dense_workspace_init(void* ws, size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t T, N, K;    /* tokens, outputs, inputs */
+  int32_t fn;         /* moe_fn */
+  int32_t dtype;      /* moe_dtype */
+  int32_t out_f32;    /* y, dx, dw, dbias in fp32 */
+  int64_t ldx;        /* pitch of x and dx */
+  int64_t ldy;        /* pitch of y and dy */
+  int64_t ldr;        /* pitch of residual */
+} moe_linear_dims;
+
+/* Bytes of workspace of the two calls below; 0 for dims that fail validation. */
+size_t moe_linear_workspace_size(const moe_linear_dims* dims);
+
+/* y = f(z) + residual, z = x W^T + bias.
+ *   x [T, K] 16-bit; w [N, K] 16-bit; bias [N] 16-bit or NULL;
+ *   residual [T, N] 16-bit or NULL; y [T, N] (out);
+ *   pre [T, N] 16-bit, packed (out): z rounded, what the backward pass of an
+ *   activation reads; or NULL. */
+moe_status moe_linear(const moe_linear_dims* dims, const void* x, const void* w, const void* bias,
+                      const void* residual, void* y, void* pre, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_linear for dy [T, N] 16-bit (the residual's is dy itself):
+ *   dz = dy f'(pre), dx = dz W [T, K], dw = dz^T x [N, K], dbias = sum_t dz [N].
+ * pre is needed exactly when fn is not MOE_FN_NONE. dx, dw and dbias may be
+ * NULL (not wanted, not all three); w is read for dx only and x for dw only,
+ * and may be NULL otherwise. dbias sums the unrounded dz. */
+moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dy, const void* x, const void* w,
+                               const void* pre, void* dx, void* dw, void* dbias,
+                               void* ws, size_t ws_bytes, void* stream);
+
+typedef struct {
+  int32_t T, H, I;    /* tokens, model width, intermediate width */
+  int32_t fn;         /* moe_fn of the gate */
+  int32_t dtype;      /* moe_dtype */
+  int32_t save;       /* moe_save */
+  int32_t out_f32;    /* y and the gradients in fp32 */
+  int32_t reserved;   /* 0 */
+  int64_t ldx;        /* pitch of x and dx */
+  int64_t ldy;        /* pitch of y and dy */
+  int64_t ldr;        /* pitch of residual */
+} moe_ffn_dims;
+
+/* Saved activations of the gated block (caller-owned, packed).
+ *   MOE_SAVE_16: g, u [T, I] 16-bit; the other fields NULL.
+ *   MOE_SAVE_8:  g, u [T, I] E4M3 codes and g_s, u_s [T, ceil(I/32)] E8M0
+ *                scales; x_q [T, H] codes and x_s [T, ceil(H/32)] scales, or
+ *                both NULL when the caller keeps x itself. */
+typedef struct {
+  void *g, *u;
+  uint8_t *g_s, *u_s;
+  uint8_t *x_q, *x_s;
+} moe_ffn_saved;
+
+size_t moe_ffn_workspace_size(const moe_ffn_dims* dims);
+
+/* y = h Wd^T + residual, h = f(g) * u, g = x Wg^T, u = x Wu^T.
+ *   x [T, H]; wg, wu [I, H]; wd [H, I]; residual [T, H] or NULL, all 16-bit;
+ *   y [T, H] (out); saved: NULL exactly when save is MOE_SAVE_NONE (its
+ *   buffers are written). */
+moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, const void* wu, const void* wd,
+                   const void* residual, void* y, const moe_ffn_saved* saved,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of moe_ffn for dy [T, H] 16-bit from what the forward pass saved
+ * (dims->save is not MOE_SAVE_NONE; g and u below are the values the saved
+ * buffers hold; the residual's gradient is dy itself):
+ *   dh = dy Wd, dg = dh u f'(g), du = dh f(g), h = f(g) u,
+ *   dx = dg Wg + du Wu [T, H], dwg = dg^T x [I, H], dwu = du^T x [I, H],
+ *   dwd = dy^T h [H, I].
+ * x [T, H] 16-bit, or NULL to read it from saved->x_q / x_s. dx, dwd and the
+ * pair dwg, dwu may be NULL (not wanted, not all of them); x is not needed
+ * without dwg and dwu. */
+moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dy, const void* x, const void* wg,
+                            const void* wu, const void* wd, const moe_ffn_saved* saved, void* dx, void* dwg,
+                            void* dwu, void* dwd, void* ws, size_t ws_bytes, void* stream);
+
+/* 8-bit activation checkpoints: OCP MX v1.0's MXFP8 with E4M3 elements, one
+ * E8M0 scale per 32 consecutive elements of a row (the last block of a row
+ * may be shorter). The scale is the smallest power of two that brings the
+ * block's largest magnitude to 448 or below (never below 2^-127), so no
+ * element saturates; elements are rounded to nearest even, zeros keep their
+ * sign. A block that holds an infinity or a NaN gets the scale code 255 and
+ * reads back as NaN.
+ *   src / dst [rows, cols] 16-bit with pitch ld (0: packed); q [rows, cols];
+ *   s [rows, ceil(cols/32)]. 1 <= rows <= 2^31 - 1; cols as N above. */
+moe_status moe_ckpt8_pack(int32_t dtype, int64_t rows, int32_t cols, const void* src, int64_t ld,
+                          uint8_t* q, uint8_t* s, void* stream);
+/* The values a checkpoint holds, rounded to 16 bits (exact for bf16 down to
+ * its smallest subnormal). */
+moe_status moe_ckpt8_unpack(int32_t dtype, int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* s,
+                            void* dst, int64_t ld, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,10 @@ __all__ = [
     "moe_selftest_bounded_wait", "STATUS_BAD_EXPERT", "STATUS_REPEATED_EXPERT",
     "STATUS_WAIT_TIMEOUT", "SCORE_SOFTMAX", "SCORE_SIGMOID", "MoeLayer", "ExpertCache",
     "moe_expert_cache_bytes",
+    "MoeLinearDims", "MoeFfnDims", "FfnSaved", "MoeFfn", "DTYPE_BF16", "DTYPE_F16", "FN_NONE", "FN_SILU",
+    "FN_GELU", "FN_RELU", "SAVE_NONE", "SAVE_16", "SAVE_8", "moe_dense_workspace_init",
+    "moe_linear_workspace_size", "moe_linear", "moe_linear_backward", "moe_ffn_workspace_size", "moe_ffn",
+    "moe_ffn_backward", "moe_ckpt8_pack", "moe_ckpt8_unpack",
 ]
 
 # bits of the device status word (moe_device_status)
@@ -109,6 +113,39 @@ _sigs.update({
                                ctypes.POINTER(ctypes.c_int64)],
     "moe_expert_ffn_streamed": [_P, _D, _P, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _Z, _P],
 })
+
+
+class MoeLinearDims(ctypes.Structure):
+    """Sizes of moe_linear / moe_linear_backward (pitches in elements, 0: packed rows)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "N", "K", "fn", "dtype", "out_f32")] + \
+               [(n, ctypes.c_int64) for n in ("ldx", "ldy", "ldr")]
+
+
+class MoeFfnDims(ctypes.Structure):
+    """Sizes of moe_ffn / moe_ffn_backward (pitches in elements, 0: packed rows)."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "H", "I", "fn", "dtype", "save", "out_f32", "reserved")] + \
+               [(n, ctypes.c_int64) for n in ("ldx", "ldy", "ldr")]
+
+
+class _FfnSavedPtrs(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("g", "u", "g_s", "u_s", "x_q", "x_s")]
+
+
+_DL = ctypes.POINTER(MoeLinearDims)
+_DF = ctypes.POINTER(MoeFfnDims)
+_DS = ctypes.POINTER(_FfnSavedPtrs)
+_sigs.update({
+    "moe_dense_workspace_init": [_P, _Z, _P],
+    "moe_linear": [_DL] + [_P] * 7 + [_Z, _P],
+    "moe_linear_backward": [_DL] + [_P] * 8 + [_Z, _P],
+    "moe_ffn": [_DF] + [_P] * 6 + [_DS, _P, _Z, _P],
+    "moe_ffn_backward": [_DF] + [_P] * 5 + [_DS] + [_P] * 5 + [_Z, _P],
+    "moe_ckpt8_pack": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, ctypes.c_int64, _P, _P, _P],
+    "moe_ckpt8_unpack": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, _P, _P, _P, ctypes.c_int64, _P],
+})
+for _n, _d in (("moe_linear_workspace_size", _DL), ("moe_ffn_workspace_size", _DF)):
+    getattr(_lib, _n).restype = ctypes.c_size_t
+    getattr(_lib, _n).argtypes = [_d]
 for _n, _a in _sigs.items():
     getattr(_lib, _n).argtypes = _a
     getattr(_lib, _n).restype = ctypes.c_int
@@ -302,6 +339,215 @@ class ExpertCache:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------------------
+# dense operators
+# ---------------------------------------------------------------------------
+
+DTYPE_BF16, DTYPE_F16 = 0, 1
+FN_NONE, FN_SILU, FN_GELU, FN_RELU = 0, 1, 2, 3
+SAVE_NONE, SAVE_16, SAVE_8 = 0, 1, 2
+
+_TORCH16 = (torch.bfloat16, torch.float16)
+
+
+def _bad(message):
+    return MoeError(1, message)
+
+
+def _tensor(t, name, dtype, shape, ld=0):
+    """Pointer of a tensor after its checks: type, shape, rows packed (or of
+    pitch ld), on the current device. The library itself sees pointers only."""
+    if t.dtype is not dtype:
+        raise _bad(f"{name} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != shape:
+        raise _bad(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if ld and ld != shape[-1]:
+        if (shape[-1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) != ld):
+            raise _bad(f"{name} has strides {t.stride()}, not ({ld}, 1)")
+    elif not t.is_contiguous():
+        raise _bad(f"{name} is not contiguous and its pitch in the dims is that of packed rows")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise _bad(f"{name} is on {t.device}, not on the current CUDA device")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, shape, ld=0):
+    return None if t is None else _tensor(t, name, dtype, shape, ld)
+
+
+def _ws_args(ws):
+    if ws.device.type != "cuda" or ws.device.index != torch.cuda.current_device() or not ws.is_contiguous():
+        raise _bad("the workspace is not a contiguous tensor on the current CUDA device")
+    return ws.data_ptr(), _nbytes(ws)
+
+
+def _types(dims):
+    """(16-bit type, output type) of dims; dims out of range are left to the library."""
+    t16 = _TORCH16[1 if dims.dtype == DTYPE_F16 else 0]
+    return t16, torch.float32 if dims.out_f32 else t16
+
+
+def moe_dense_workspace_init(ws, stream=None):
+    p, n = _ws_args(ws)
+    _check(_lib.moe_dense_workspace_init(p, n, _stream(stream)))
+
+
+def _size(fn, dims):
+    n = fn(ctypes.byref(dims))
+    if n == 0:
+        raise MoeError(2, _lib.moe_last_error().decode())
+    return n
+
+
+def moe_linear_workspace_size(dims: MoeLinearDims) -> int:
+    """Bytes of workspace (raises for dims the library does not support)."""
+    return _size(_lib.moe_linear_workspace_size, dims)
+
+
+def moe_ffn_workspace_size(dims: MoeFfnDims) -> int:
+    """Bytes of workspace (raises for dims the library does not support)."""
+    return _size(_lib.moe_ffn_workspace_size, dims)
+
+
+def moe_linear(dims, x, w, bias, residual, y, pre, ws, stream=None):
+    """y = f(x W^T + bias) + residual; pre (or None) receives the argument of f."""
+    t16, out = _types(dims)
+    T, N, K = dims.T, dims.N, dims.K
+    wp, wn = _ws_args(ws)
+    _check(_lib.moe_linear(
+        ctypes.byref(dims), _tensor(x, "x", t16, (T, K), dims.ldx), _tensor(w, "w", t16, (N, K)),
+        _opt(bias, "bias", t16, (N,)), _opt(residual, "residual", t16, (T, N), dims.ldr),
+        _tensor(y, "y", out, (T, N), dims.ldy), _opt(pre, "pre", t16, (T, N)), wp, wn, _stream(stream)))
+
+
+def moe_linear_backward(dims, dy, x, w, pre, dx, dw, dbias, ws, stream=None):
+    """Gradients of moe_linear; dx, dw and dbias may each be None (not wanted)."""
+    t16, out = _types(dims)
+    T, N, K = dims.T, dims.N, dims.K
+    wp, wn = _ws_args(ws)
+    _check(_lib.moe_linear_backward(
+        ctypes.byref(dims), _tensor(dy, "dy", t16, (T, N), dims.ldy), _opt(x, "x", t16, (T, K), dims.ldx),
+        _opt(w, "w", t16, (N, K)), _opt(pre, "pre", t16, (T, N)), _opt(dx, "dx", out, (T, K), dims.ldx),
+        _opt(dw, "dw", out, (N, K)), _opt(dbias, "dbias", out, (N,)), wp, wn, _stream(stream)))
+
+
+class FfnSaved:
+    """Saved activations of moe_ffn: g and u in 16 bits (SAVE_16), or g, u and
+    x as 8-bit checkpoints (SAVE_8; keep_x=False when the caller keeps x
+    itself). Buffers that are not given are allocated."""
+
+    def __init__(self, dims: MoeFfnDims, g=None, u=None, keep_x=True, device="cuda"):
+        T, H, I = dims.T, dims.H, dims.I
+        self.g_s = self.u_s = self.x_q = self.x_s = None
+        u8 = dict(dtype=torch.uint8, device=device)
+        if dims.save == SAVE_16:
+            t16 = _types(dims)[0]
+            kind = dict(dtype=t16, device=device)
+        elif dims.save == SAVE_8:
+            kind = u8
+            self.g_s = torch.empty(T, (I + 31) // 32, **u8)
+            self.u_s = torch.empty(T, (I + 31) // 32, **u8)
+            if keep_x:
+                self.x_q = torch.empty(T, H, **u8)
+                self.x_s = torch.empty(T, (H + 31) // 32, **u8)
+        else:
+            raise _bad("dims.save is SAVE_NONE: there is nothing to save")
+        self.g = torch.empty(T, I, **kind) if g is None else g
+        self.u = torch.empty(T, I, **kind) if u is None else u
+
+    def _ptrs(self, dims):
+        T, H, I = dims.T, dims.H, dims.I
+        t = torch.uint8 if dims.save == SAVE_8 else _types(dims)[0]
+        ni, nh = (I + 31) // 32, (H + 31) // 32
+        u8 = torch.uint8
+        return _FfnSavedPtrs(
+            g=_tensor(self.g, "saved.g", t, (T, I)), u=_tensor(self.u, "saved.u", t, (T, I)),
+            g_s=_opt(self.g_s, "saved.g_s", u8, (T, ni)), u_s=_opt(self.u_s, "saved.u_s", u8, (T, ni)),
+            x_q=_opt(self.x_q, "saved.x_q", u8, (T, H)), x_s=_opt(self.x_s, "saved.x_s", u8, (T, nh)))
+
+
+def _saved(saved, dims):
+    return None if saved is None else ctypes.byref(saved._ptrs(dims))
+
+
+def moe_ffn(dims, x, wg, wu, wd, residual, y, saved, ws, stream=None):
+    """y = (f(x Wg^T) * (x Wu^T)) Wd^T + residual; saved: an FfnSaved, or None with SAVE_NONE."""
+    t16, out = _types(dims)
+    T, H, I = dims.T, dims.H, dims.I
+    wp, wn = _ws_args(ws)
+    _check(_lib.moe_ffn(
+        ctypes.byref(dims), _tensor(x, "x", t16, (T, H), dims.ldx), _tensor(wg, "wg", t16, (I, H)),
+        _tensor(wu, "wu", t16, (I, H)), _tensor(wd, "wd", t16, (H, I)),
+        _opt(residual, "residual", t16, (T, H), dims.ldr), _tensor(y, "y", out, (T, H), dims.ldy),
+        _saved(saved, dims), wp, wn, _stream(stream)))
+
+
+def moe_ffn_backward(dims, dy, x, wg, wu, wd, saved, dx, dwg, dwu, dwd, ws, stream=None):
+    """Gradients of moe_ffn from `saved` (x None: from its 8-bit checkpoint);
+    dx, dwd and the pair dwg, dwu may be None (not wanted)."""
+    t16, out = _types(dims)
+    T, H, I = dims.T, dims.H, dims.I
+    wp, wn = _ws_args(ws)
+    _check(_lib.moe_ffn_backward(
+        ctypes.byref(dims), _tensor(dy, "dy", t16, (T, H), dims.ldy), _opt(x, "x", t16, (T, H), dims.ldx),
+        _opt(wg, "wg", t16, (I, H)), _opt(wu, "wu", t16, (I, H)), _tensor(wd, "wd", t16, (H, I)),
+        _saved(saved, dims), _opt(dx, "dx", out, (T, H), dims.ldx), _opt(dwg, "dwg", out, (I, H)),
+        _opt(dwu, "dwu", out, (I, H)), _opt(dwd, "dwd", out, (H, I)), wp, wn, _stream(stream)))
+
+
+def _rows16(t, name):
+    if t.dim() != 2 or t.dtype not in _TORCH16:
+        raise _bad(f"{name} is not a 2-D bf16 or f16 tensor")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    return _TORCH16.index(t.dtype), rows, cols, ld, _tensor(t, name, t.dtype, (rows, cols), ld)
+
+
+def moe_ckpt8_pack(src, q, s, stream=None):
+    """src [rows, cols] (bf16 or f16, any row pitch) -> E4M3 codes q [rows, cols]
+    and E8M0 scales s [rows, ceil(cols / 32)], both uint8."""
+    dt, rows, cols, ld, p = _rows16(src, "src")
+    _check(_lib.moe_ckpt8_pack(dt, rows, cols, p, ld, _tensor(q, "q", torch.uint8, (rows, cols)),
+                               _tensor(s, "s", torch.uint8, (rows, (cols + 31) // 32)), _stream(stream)))
+
+
+def moe_ckpt8_unpack(q, s, dst, stream=None):
+    """The values an 8-bit checkpoint holds, into dst [rows, cols] (bf16 or f16)."""
+    dt, rows, cols, ld, p = _rows16(dst, "dst")
+    _check(_lib.moe_ckpt8_unpack(dt, rows, cols, _tensor(q, "q", torch.uint8, (rows, cols)),
+                                 _tensor(s, "s", torch.uint8, (rows, (cols + 31) // 32)), p, ld, _stream(stream)))
+
+
+class MoeFfn:
+    """Owns the device buffers of one gated feed-forward block (packed rows)
+    and calls the C ABI on them. ``weights``: wg, wu [I, H] and wd [H, I]."""
+
+    def __init__(self, dims: MoeFfnDims, weights: dict, device="cuda"):
+        self.dims = dims
+        self.w = {n: weights[n] for n in ("wg", "wu", "wd")}
+        self.ws = torch.empty(moe_ffn_workspace_size(dims), dtype=torch.uint8, device=device)
+        moe_dense_workspace_init(self.ws)
+        t16, out = _types(dims)
+        self.y = torch.empty(dims.T, dims.H, dtype=out, device=device)
+        self.saved = None
+        if dims.save != SAVE_NONE:
+            self.saved = FfnSaved(dims, device=device)
+            self.dx = torch.empty_like(self.y)
+            self.dw = {n: torch.empty(w.shape, dtype=out, device=device) for n, w in self.w.items()}
+
+    def __call__(self, x, residual=None, stream=None):
+        w = self.w
+        moe_ffn(self.dims, x, w["wg"], w["wu"], w["wd"], residual, self.y, self.saved, self.ws, stream)
+        return self.y
+
+    def backward(self, dy, x=None, stream=None):
+        """(dx, {wg, wu, wd gradients}) of the last call; x is needed with SAVE_16."""
+        w, dw = self.w, self.dw
+        moe_ffn_backward(self.dims, dy, x, w["wg"], w["wu"], w["wd"], self.saved, self.dx, dw["wg"], dw["wu"],
+                         dw["wd"], self.ws, stream)
+        return self.dx, dw
 
 
 # ---------------------------------------------------------------------------

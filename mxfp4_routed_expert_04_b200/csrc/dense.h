@@ -1,0 +1,82 @@
+// Internal interfaces of the dense operators: the projection with a fused
+// epilogue (moe_linear), the gated feed-forward block (moe_ffn), their backward
+// passes and the 8-bit activation checkpoints.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/moe_mxfp4.h"
+
+namespace moe {
+
+
+// --- tiled GEMM (dense_gemm.cu) -----------------------------------------------
+// D[M, N] = sum over segments of A_s B_s with the epilogue of `kEpi`:
+enum DenseEpi {
+  kEpiLinear = 0,   // y = f(D + bias) + residual (and the f argument, for the backward pass)
+  kEpiGlu = 1,      // D holds gate and up columns side by side: h = f(g) * u (and g, u saved)
+  kEpiDGlu = 2,     // D = dh: dg = dh u f'(g), du = dh f(g), h = f(g) u
+};
+
+struct DenseGemmArgs {
+  // A and B of the contraction segments (dX of the gated block: dG Wg + dU Wu),
+  // or A of the row segments (dWg and dWu share B), or B of the gate and up halves
+  CUtensorMap map_a[2], map_b[2];
+  int M, N, K;              // rows of one row segment, output columns (h columns for kEpiGlu), contraction
+  int k_segs;               // contraction segments (1 or 2)
+  int m_segs;               // row segments (1 or 2), each M rows with its own A and output
+  int tile_n;               // columns of a tile (accumulator columns), a multiple of 64 up to 256
+  int f16;                  // 16-bit type: 0 bf16, 1 f16
+  int fn;                   // moe_fn
+  int out_f32;              // out[] in fp32 instead of the 16-bit type
+  int saved8;               // kEpiGlu writes / kEpiDGlu reads g and u as 8-bit checkpoints
+  const void* bias;         // [N] 16-bit or NULL
+  const void* residual;     // [M, ldr] 16-bit or NULL
+  void* out[2];             // kEpiLinear: per row segment; kEpiGlu: h; kEpiDGlu: dg, du
+  void* pre;                // kEpiLinear: D + bias [M, N] 16-bit or NULL; kEpiDGlu: h
+  void* g;                  // kEpiGlu out (or NULL) / kEpiDGlu in: [M, N] 16-bit, or E4M3 codes
+  void* u;
+  uint8_t* g_s;             // E8M0 scales [M, ceil(N/32)] of the codes
+  uint8_t* u_s;
+  int64_t ldr, ldo;         // row pitches in elements
+  int32_t* status;
+};
+
+template <int kEpi, bool kAMn, bool kBMn, int kCg>
+__global__ void k_dense_gemm(const __grid_constant__ DenseGemmArgs a);
+size_t dense_gemm_smem_bytes(int cg);
+int dense_gemm_threads();
+
+// --- element kernels (dense_elem.cu) ------------------------------------------
+// dz = dy * f'(pre) rounded to 16 bits (dz NULL: not written; pre NULL: f' = 1)
+// and, per chunk of `rows` rows, the column sums of the unrounded dz
+struct DzArgs {
+  const void* dy;
+  const void* pre;
+  void* dz;
+  float* part;              // [chunks, N] or NULL
+  int T, N, rows, f16, fn;
+  int64_t lddy;
+};
+__global__ void k_dz(DzArgs a);
+constexpr int kDzCols = 256, kDzThreads = 256;
+// out[n] = sum over chunks, in order
+__global__ void k_colsum(const float* part, int chunks, int N, int f16, int out_f32, void* out);
+
+// 16-bit rows -> E4M3 codes with one E8M0 scale per 32 elements of a row, and back
+struct Ckpt8Args {
+  const void* src;
+  void* dst;
+  uint8_t* q;
+  uint8_t* s;
+  int64_t rows, ld;         // ld: row pitch of the 16-bit side, in elements
+  int cols, f16;
+};
+__global__ void k_ckpt8_pack(Ckpt8Args a);
+__global__ void k_ckpt8_unpack(Ckpt8Args a);
+constexpr int kCkptThreads = 256;
+
+}  // namespace moe

@@ -1,0 +1,535 @@
+// C ABI of the dense operators: validation, workspace plan, launch order.
+// Declared in include/moe_mxfp4.h.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdarg.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "../../include/moe_mxfp4.h"
+#include "dense.h"
+#include "kernels.h"
+
+namespace {
+
+moe_status fail(moe_status s, const char* fmt, ...) {
+  char msg[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  return moe::record_error(s, msg);
+}
+
+inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
+
+#define NEED(p)                                                                         \
+  do {                                                                                  \
+    if (!(p)) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", #p);                       \
+    if (!aligned16(p)) return fail(MOE_ERR_ALIGNMENT, "%s is not 16-byte aligned", #p); \
+  } while (0)
+#define MAYBE(p)                                                                        \
+  do {                                                                                  \
+    if (!aligned16(p)) return fail(MOE_ERR_ALIGNMENT, "%s is not 16-byte aligned", #p); \
+  } while (0)
+#define TRY(e)                         \
+  do {                                 \
+    const moe_status s_ = (e);         \
+    if (s_ != MOE_OK) return s_;       \
+  } while (0)
+
+constexpr size_t kStatusBytes = 256;
+
+moe_status check_width(const char* name, int v) {
+  if (v < 8 || v > 65536 || v % 8 != 0)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s=%d is not a multiple of 8 in [8, 65536]", name, v);
+  return MOE_OK;
+}
+moe_status check_common(int T, int fn, int dtype, int out_f32) {
+  if (T < 1 || T > 65536) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T=%d outside [1, 65536]", T);
+  if (fn < MOE_FN_NONE || fn > MOE_FN_RELU) return fail(MOE_ERR_INVALID_ARG, "fn %d is not a moe_fn", fn);
+  if (dtype != MOE_BF16 && dtype != MOE_F16) return fail(MOE_ERR_INVALID_ARG, "dtype %d is not a moe_dtype", dtype);
+  if (out_f32 != 0 && out_f32 != 1) return fail(MOE_ERR_INVALID_ARG, "out_f32 %d is not 0 or 1", out_f32);
+  return MOE_OK;
+}
+// a row pitch (0: packed) into *out
+moe_status check_pitch(const char* name, int64_t ld, int cols, int64_t* out) {
+  if (ld == 0) ld = cols;
+  if (ld < cols || ld % 8 != 0 || ld >= ((int64_t)1 << 31))
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%s=%lld is not a multiple of 8 in [%d, 2^31)", name, (long long)ld, cols);
+  *out = ld;
+  return MOE_OK;
+}
+moe_status check_ws(void* ws, size_t ws_bytes, size_t need) {
+  if (!ws) return fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  if (!aligned16(ws)) return fail(MOE_ERR_ALIGNMENT, "workspace not 16-byte aligned");
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < %zu needed", ws_bytes, need);
+  return MOE_OK;
+}
+
+moe_status launched(cudaError_t e, const char* what) {
+  const cudaError_t last = cudaGetLastError();
+  if (e == cudaSuccess) e = last;
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+// --- plans --------------------------------------------------------------------
+
+struct LinearPlan {
+  int T, N, K, fn, f16, out_f32;
+  int64_t ldx, ldy, ldr;
+  int dz_rows, dz_chunks;       // row chunks of the bias gradient's partial sums
+  size_t off_dz, off_part, total;
+};
+// rows of a bias-gradient chunk: at most 128 chunks, at least 64 rows each
+int dz_chunk_rows(int T) { return std::max(64, (T + 127) / 128); }
+
+moe_status make_plan(const moe_linear_dims* d, LinearPlan& p) {
+  if (!d) return fail(MOE_ERR_INVALID_ARG, "dims is NULL");
+  TRY(check_common(d->T, d->fn, d->dtype, d->out_f32));
+  TRY(check_width("N", d->N));
+  TRY(check_width("K", d->K));
+  p.T = d->T; p.N = d->N; p.K = d->K; p.fn = d->fn; p.f16 = d->dtype; p.out_f32 = d->out_f32;
+  TRY(check_pitch("ldx", d->ldx, d->K, &p.ldx));
+  TRY(check_pitch("ldy", d->ldy, d->N, &p.ldy));
+  TRY(check_pitch("ldr", d->ldr, d->N, &p.ldr));
+  p.dz_rows = dz_chunk_rows(p.T);
+  p.dz_chunks = (p.T + p.dz_rows - 1) / p.dz_rows;
+  size_t o = kStatusBytes;
+  p.off_dz = o;
+  o = align_up(o + (p.fn ? (size_t)p.T * p.N * 2 : 0), 256);
+  p.off_part = o;
+  o = align_up(o + (size_t)p.dz_chunks * p.N * 4, 256);
+  p.total = o;
+  return MOE_OK;
+}
+
+struct FfnPlan {
+  int T, H, I, fn, f16, save, out_f32;
+  int64_t ldx, ldy, ldr;
+  size_t off_h, off_dg, off_du, off_x, total;
+};
+
+moe_status make_plan(const moe_ffn_dims* d, FfnPlan& p) {
+  if (!d) return fail(MOE_ERR_INVALID_ARG, "dims is NULL");
+  TRY(check_common(d->T, d->fn, d->dtype, d->out_f32));
+  TRY(check_width("H", d->H));
+  TRY(check_width("I", d->I));
+  if (d->save < MOE_SAVE_NONE || d->save > MOE_SAVE_8)
+    return fail(MOE_ERR_INVALID_ARG, "save %d is not a moe_save", d->save);
+  if (d->reserved != 0) return fail(MOE_ERR_INVALID_ARG, "reserved is not 0");
+  p.T = d->T; p.H = d->H; p.I = d->I; p.fn = d->fn; p.f16 = d->dtype; p.save = d->save; p.out_f32 = d->out_f32;
+  TRY(check_pitch("ldx", d->ldx, d->H, &p.ldx));
+  TRY(check_pitch("ldy", d->ldy, d->H, &p.ldy));
+  TRY(check_pitch("ldr", d->ldr, d->H, &p.ldr));
+  const size_t hidden = align_up((size_t)p.T * p.I * 2, 256);
+  size_t o = kStatusBytes;
+  p.off_h = o;
+  o += hidden;
+  p.off_dg = o;
+  if (p.save != MOE_SAVE_NONE) o += hidden;
+  p.off_du = o;
+  if (p.save != MOE_SAVE_NONE) o += hidden;
+  p.off_x = o;
+  if (p.save == MOE_SAVE_8) o += align_up((size_t)p.T * p.H * 2, 256);
+  p.total = o;
+  return MOE_OK;
+}
+
+// --- device ----------------------------------------------------------------------
+
+struct Device {
+  bool ready = false;
+  int num_sms = 0;
+};
+std::mutex g_mu;
+Device g_dev[64];
+
+template <int kEpi, bool kAMn, bool kBMn, int kCg>
+cudaError_t allow_smem() {
+  return cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, kAMn, kBMn, kCg>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)moe::dense_gemm_smem_bytes(kCg));
+}
+
+moe_status device(const Device** out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+    return fail(MOE_ERR_CUDA, "cudaGetDevice failed");
+  std::lock_guard<std::mutex> lk(g_mu);
+  Device& s = g_dev[dev];
+  if (!s.ready) {
+    cudaError_t e = cudaDeviceGetAttribute(&s.num_sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, false, 1>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, true, 1>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, true, true, 1>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu, false, false, 1>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu, false, true, 1>();
+    if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "device setup: %s", cudaGetErrorString(e));
+    s.ready = true;
+  }
+  *out = &s;
+  return MOE_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// 16-bit matrix [rows, cols] with row pitch ld, read in boxes of box_rows rows
+// x 64 elements with the 128-byte swizzle
+moe_status map16(CUtensorMap* m, const void* base, int f16, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+                 const char* what) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "tensor map for %s: CUresult %d", what, (int)r);
+  return MOE_OK;
+}
+
+// Launch with programmatic stream serialization (every kernel waits in
+// pdl_wait() before it touches memory) and clusters of `cg` CTAs.
+template <typename... KArgs, typename... Args>
+moe_status launch(const char* what, void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int cg,
+                  cudaStream_t st, Args... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cg;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cg > 1 ? 2 : 1;
+  return launched(cudaLaunchKernelEx(&cfg, kernel, args...), what);
+}
+
+// --- products ----------------------------------------------------------------------
+
+// An operand: a packed or pitched row-major matrix
+struct Mat {
+  const void* p;
+  int64_t rows, cols, ld;
+};
+
+template <int kEpi, bool kAMn, bool kBMn>
+moe_status gemm(const Device& dv, moe::DenseGemmArgs& g, const Mat* a, int na, const Mat* b, int nb, int tile_n,
+                cudaStream_t st, const char* what) {
+  constexpr int cg = 1;
+  g.tile_n = tile_n;
+  for (int i = 0; i < na; ++i)
+    TRY(map16(&g.map_a[i], a[i].p, g.f16, a[i].rows, a[i].cols, a[i].ld, kAMn ? 64 : 128, what));
+  for (int i = 0; i < nb; ++i)
+    TRY(map16(&g.map_b[i], b[i].p, g.f16, b[i].rows, b[i].cols, b[i].ld,
+              kBMn ? 64 : kEpi == moe::kEpiGlu ? tile_n / 2 : tile_n / cg, what));
+  const int cols = kEpi == moe::kEpiGlu ? tile_n / 2 : tile_n;
+  const long tiles = (long)g.m_segs * ((g.M + 128 * cg - 1) / (128 * cg)) * ((g.N + cols - 1) / cols);
+  const int ctas = (int)std::min<long>(tiles, dv.num_sms / cg) * cg;
+  return launch(what, moe::k_dense_gemm<kEpi, kAMn, kBMn, cg>, dim3((unsigned)ctas), moe::dense_gemm_threads(),
+                moe::dense_gemm_smem_bytes(cg), cg, st, g);
+}
+
+moe::DenseGemmArgs gemm_args(int M, int N, int K, int f16, void* ws) {
+  moe::DenseGemmArgs g;
+  memset(&g, 0, sizeof(g));
+  g.M = M; g.N = N; g.K = K; g.f16 = f16;
+  g.k_segs = 1; g.m_segs = 1;
+  g.status = static_cast<int32_t*>(ws);
+  return g;
+}
+
+int pick_tile_n(int N) { return N > 128 ? 256 : N > 64 ? 128 : 64; }
+
+// y[T, N] = f(x W^T + bias) + residual
+moe_status project(const Device& dv, int T, int N, int K, int f16, int fn, int out_f32, const void* x, int64_t ldx,
+                   const void* w, const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                   void* pre, void* ws, cudaStream_t st, const char* what) {
+  moe::DenseGemmArgs g = gemm_args(T, N, K, f16, ws);
+  g.fn = fn; g.out_f32 = out_f32; g.bias = bias; g.residual = residual; g.ldr = ldr;
+  g.out[0] = y; g.ldo = ldy; g.pre = pre;
+  const Mat a = {x, T, K, ldx}, b = {w, N, K, K};
+  return gemm<moe::kEpiLinear, false, false>(dv, g, &a, 1, &b, 1, pick_tile_n(N), st, what);
+}
+
+// dx[T, K] = sum_s dz_s[T, N] W_s[N, K]
+moe_status input_grad(const Device& dv, int T, int N, int K, int f16, int out_f32, const Mat* dz, const Mat* w,
+                      int segs, void* dx, int64_t lddx, void* ws, cudaStream_t st, const char* what) {
+  moe::DenseGemmArgs g = gemm_args(T, K, N, f16, ws);
+  g.k_segs = segs; g.out_f32 = out_f32; g.out[0] = dx; g.ldo = lddx;
+  return gemm<moe::kEpiLinear, false, true>(dv, g, dz, segs, w, segs, pick_tile_n(K), st, what);
+}
+
+// dw_s[N, K] = dz_s[T, N]^T x[T, K]
+moe_status weight_grad(const Device& dv, int T, int N, int K, int f16, int out_f32, const Mat* dz, int segs,
+                       const Mat& x, void* dw0, void* dw1, void* ws, cudaStream_t st, const char* what) {
+  moe::DenseGemmArgs g = gemm_args(N, K, T, f16, ws);
+  g.m_segs = segs; g.out_f32 = out_f32; g.out[0] = dw0; g.out[1] = dw1; g.ldo = K;
+  return gemm<moe::kEpiLinear, true, true>(dv, g, dz, segs, &x, 1, pick_tile_n(K), st, what);
+}
+
+moe_status ckpt8(const Device& dv, bool pack, int f16, int64_t rows, int cols, const void* src, void* dst, int64_t ld,
+                 uint8_t* q, uint8_t* s, cudaStream_t st) {
+  moe::Ckpt8Args c;
+  c.src = src; c.dst = dst; c.q = q; c.s = s; c.rows = rows; c.ld = ld; c.cols = cols; c.f16 = f16;
+  const int64_t items = rows * (pack ? (cols + 31) / 32 : cols / 8);
+  const int64_t blocks = std::min<int64_t>((items + moe::kCkptThreads - 1) / moe::kCkptThreads,
+                                           (int64_t)dv.num_sms * 16);
+  return launch(pack ? "checkpoint pack" : "checkpoint unpack", pack ? moe::k_ckpt8_pack : moe::k_ckpt8_unpack,
+                dim3((unsigned)blocks), moe::kCkptThreads, 0, 1, st, c);
+}
+
+moe_status check_ckpt8(int32_t dtype, int64_t rows, int32_t cols, const void* x, int64_t* ld, const void* q,
+                       const void* s, const char* name) {
+  if (dtype != MOE_BF16 && dtype != MOE_F16) return fail(MOE_ERR_INVALID_ARG, "dtype %d is not a moe_dtype", dtype);
+  if (rows < 1 || rows > 0x7FFFFFFF)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rows=%lld outside [1, 2^31 - 1]", (long long)rows);
+  TRY(check_width("cols", cols));
+  TRY(check_pitch("ld", *ld, cols, ld));
+  if (!x) return fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned16(x)) return fail(MOE_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
+  NEED(q);
+  NEED(s);
+  return MOE_OK;
+}
+
+// the saved buffers that `save` asks for
+moe_status check_saved(const FfnPlan& p, const moe_ffn_saved* saved) {
+  if (p.save == MOE_SAVE_NONE) {
+    if (saved) return fail(MOE_ERR_INVALID_ARG, "saved is not NULL, but save is MOE_SAVE_NONE");
+    return MOE_OK;
+  }
+  if (!saved) return fail(MOE_ERR_INVALID_ARG, "saved is NULL");
+  NEED(saved->g);
+  NEED(saved->u);
+  if (p.save == MOE_SAVE_8) {
+    NEED(saved->g_s);
+    NEED(saved->u_s);
+    if (!saved->x_q != !saved->x_s)
+      return fail(MOE_ERR_INVALID_ARG, "saved->x_q and saved->x_s: both or neither");
+    MAYBE(saved->x_q);
+    MAYBE(saved->x_s);
+  } else if (saved->g_s || saved->u_s || saved->x_q || saved->x_s) {
+    return fail(MOE_ERR_INVALID_ARG, "saved scales or x codes with MOE_SAVE_16");
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+// ===========================================================================
+// C ABI
+// ===========================================================================
+extern "C" {
+
+moe_status moe_dense_workspace_init(void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_ws(ws, ws_bytes, kStatusBytes));
+  const cudaError_t e = cudaMemsetAsync(ws, 0, kStatusBytes, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "status clear: %s", cudaGetErrorString(e));
+  return MOE_OK;
+}
+
+size_t moe_linear_workspace_size(const moe_linear_dims* dims) {
+  LinearPlan p;
+  return make_plan(dims, p) == MOE_OK ? p.total : 0;
+}
+
+size_t moe_ffn_workspace_size(const moe_ffn_dims* dims) {
+  FfnPlan p;
+  return make_plan(dims, p) == MOE_OK ? p.total : 0;
+}
+
+moe_status moe_linear(const moe_linear_dims* dims, const void* x, const void* w, const void* bias,
+                      const void* residual, void* y, void* pre, void* ws, size_t ws_bytes, void* stream) {
+  LinearPlan p;
+  TRY(make_plan(dims, p));
+  NEED(x);
+  NEED(w);
+  NEED(y);
+  MAYBE(bias);
+  MAYBE(residual);
+  MAYBE(pre);
+  if (y == residual && (p.out_f32 || p.ldy != p.ldr))
+    return fail(MOE_ERR_INVALID_ARG, "y is the residual, but not of its type and pitch");
+  TRY(check_ws(ws, ws_bytes, p.total));
+  const Device* dv;
+  TRY(device(&dv));
+  return project(*dv, p.T, p.N, p.K, p.f16, p.fn, p.out_f32, x, p.ldx, w, bias, residual, p.ldr, y, p.ldy, pre, ws,
+                 (cudaStream_t)stream, "projection");
+}
+
+moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dy, const void* x, const void* w,
+                               const void* pre, void* dx, void* dw, void* dbias,
+                               void* ws, size_t ws_bytes, void* stream) {
+  LinearPlan p;
+  TRY(make_plan(dims, p));
+  NEED(dy);
+  if (!dx && !dw && !dbias) return fail(MOE_ERR_INVALID_ARG, "dx, dw and dbias are all NULL");
+  if (dx) NEED(w);
+  if (dw) NEED(x);
+  if (p.fn) NEED(pre);
+  if (!p.fn && pre) return fail(MOE_ERR_INVALID_ARG, "pre is not NULL, but fn is MOE_FN_NONE");
+  MAYBE(dx);
+  MAYBE(dw);
+  MAYBE(dbias);
+  TRY(check_ws(ws, ws_bytes, p.total));
+  const Device* dv;
+  TRY(device(&dv));
+  cudaStream_t st = (cudaStream_t)stream;
+  Mat dz = {dy, p.T, p.N, p.ldy};
+  if (p.fn || dbias) {
+    moe::DzArgs z;
+    z.dy = dy; z.pre = pre; z.lddy = p.ldy;
+    z.dz = p.fn && (dx || dw) ? at(ws, p.off_dz) : nullptr;
+    z.part = dbias ? reinterpret_cast<float*>(at(ws, p.off_part)) : nullptr;
+    z.T = p.T; z.N = p.N; z.rows = p.dz_rows; z.f16 = p.f16; z.fn = p.fn;
+    TRY(launch("activation gradient", moe::k_dz,
+               dim3((unsigned)((p.N + moe::kDzCols - 1) / moe::kDzCols), (unsigned)p.dz_chunks), moe::kDzThreads, 0, 1,
+               st, z));
+    if (dbias)
+      TRY(launch("bias gradient", moe::k_colsum, dim3((unsigned)((p.N + 255) / 256)), 256, 0, 1, st,
+                 (const float*)z.part, p.dz_chunks, p.N, p.f16, p.out_f32, dbias));
+    if (z.dz) dz = {z.dz, p.T, p.N, p.N};
+  }
+  if (dx) {
+    const Mat wm = {w, p.N, p.K, p.K};
+    TRY(input_grad(*dv, p.T, p.N, p.K, p.f16, p.out_f32, &dz, &wm, 1, dx, p.ldx, ws, st, "input gradient"));
+  }
+  if (dw) {
+    const Mat xm = {x, p.T, p.K, p.ldx};
+    TRY(weight_grad(*dv, p.T, p.N, p.K, p.f16, p.out_f32, &dz, 1, xm, dw, nullptr, ws, st, "weight gradient"));
+  }
+  return MOE_OK;
+}
+
+moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, const void* wu, const void* wd,
+                   const void* residual, void* y, const moe_ffn_saved* saved,
+                   void* ws, size_t ws_bytes, void* stream) {
+  FfnPlan p;
+  TRY(make_plan(dims, p));
+  NEED(x);
+  NEED(wg);
+  NEED(wu);
+  NEED(wd);
+  NEED(y);
+  MAYBE(residual);
+  if (y == residual && (p.out_f32 || p.ldy != p.ldr))
+    return fail(MOE_ERR_INVALID_ARG, "y is the residual, but not of its type and pitch");
+  TRY(check_saved(p, saved));
+  TRY(check_ws(ws, ws_bytes, p.total));
+  const Device* dv;
+  TRY(device(&dv));
+  cudaStream_t st = (cudaStream_t)stream;
+  void* h = at(ws, p.off_h);
+  moe::DenseGemmArgs g = gemm_args(p.T, p.I, p.H, p.f16, ws);
+  g.fn = p.fn; g.out[0] = h;
+  if (saved) {
+    g.g = saved->g; g.u = saved->u; g.g_s = saved->g_s; g.u_s = saved->u_s;
+    g.saved8 = p.save == MOE_SAVE_8;
+  }
+  const Mat xm = {x, p.T, p.H, p.ldx};
+  const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}};
+  TRY((gemm<moe::kEpiGlu, false, false>(*dv, g, &xm, 1, wm, 2, p.I > 64 ? 256 : 128, st, "gate/up projection")));
+  if (saved && saved->x_q)
+    TRY(ckpt8(*dv, true, p.f16, p.T, p.H, x, nullptr, p.ldx, saved->x_q, saved->x_s, st));
+  return project(*dv, p.T, p.H, p.I, p.f16, MOE_FN_NONE, p.out_f32, h, p.I, wd, nullptr, residual, p.ldr, y, p.ldy,
+                 nullptr, ws, st, "down projection");
+}
+
+moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dy, const void* x, const void* wg,
+                            const void* wu, const void* wd, const moe_ffn_saved* saved, void* dx, void* dwg,
+                            void* dwu, void* dwd, void* ws, size_t ws_bytes, void* stream) {
+  FfnPlan p;
+  TRY(make_plan(dims, p));
+  if (p.save == MOE_SAVE_NONE) return fail(MOE_ERR_INVALID_ARG, "save is MOE_SAVE_NONE: nothing to go back from");
+  NEED(dy);
+  NEED(wd);
+  if (!dwg != !dwu) return fail(MOE_ERR_INVALID_ARG, "dwg and dwu: both or neither");
+  if (!dx && !dwg && !dwd) return fail(MOE_ERR_INVALID_ARG, "dx, dwg, dwu and dwd are all NULL");
+  if (dx) {
+    NEED(wg);
+    NEED(wu);
+  }
+  MAYBE(x);
+  MAYBE(dx);
+  MAYBE(dwg);
+  MAYBE(dwu);
+  MAYBE(dwd);
+  TRY(check_saved(p, saved));
+  if (dwg && !x && !saved->x_q)
+    return fail(MOE_ERR_INVALID_ARG, "x is NULL and saved holds no x_q: the weight gradients need one");
+  TRY(check_ws(ws, ws_bytes, p.total));
+  const Device* dv;
+  TRY(device(&dv));
+  cudaStream_t st = (cudaStream_t)stream;
+  const Mat dym = {dy, p.T, p.H, p.ldy};
+  Mat xm = {x, p.T, p.H, p.ldx};
+  if (dwg && !x) {
+    TRY(ckpt8(*dv, false, p.f16, p.T, p.H, nullptr, at(ws, p.off_x), p.H, saved->x_q, saved->x_s, st));
+    xm = {at(ws, p.off_x), p.T, p.H, p.H};
+  }
+  moe::DenseGemmArgs g = gemm_args(p.T, p.I, p.H, p.f16, ws);
+  g.fn = p.fn; g.saved8 = p.save == MOE_SAVE_8;
+  g.g = saved->g; g.u = saved->u; g.g_s = saved->g_s; g.u_s = saved->u_s;
+  g.out[0] = at(ws, p.off_dg); g.out[1] = at(ws, p.off_du); g.pre = at(ws, p.off_h);
+  const Mat wdm = {wd, p.H, p.I, p.I};
+  TRY((gemm<moe::kEpiDGlu, false, true>(*dv, g, &dym, 1, &wdm, 1, pick_tile_n(p.I), st, "hidden gradient")));
+  const Mat dgu[2] = {{g.out[0], p.T, p.I, p.I}, {g.out[1], p.T, p.I, p.I}};
+  if (dx) {
+    const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}};
+    TRY(input_grad(*dv, p.T, p.I, p.H, p.f16, p.out_f32, dgu, wm, 2, dx, p.ldx, ws, st, "input gradient"));
+  }
+  if (dwg)
+    TRY(weight_grad(*dv, p.T, p.I, p.H, p.f16, p.out_f32, dgu, 2, xm, dwg, dwu, ws, st, "gate/up weight gradient"));
+  if (dwd) {
+    const Mat hm = {g.pre, p.T, p.I, p.I};
+    TRY(weight_grad(*dv, p.T, p.H, p.I, p.f16, p.out_f32, &dym, 1, hm, dwd, nullptr, ws, st, "down weight gradient"));
+  }
+  return MOE_OK;
+}
+
+moe_status moe_ckpt8_pack(int32_t dtype, int64_t rows, int32_t cols, const void* src, int64_t ld,
+                          uint8_t* q, uint8_t* s, void* stream) {
+  TRY(check_ckpt8(dtype, rows, cols, src, &ld, q, s, "src"));
+  const Device* dv;
+  TRY(device(&dv));
+  return ckpt8(*dv, true, dtype, rows, cols, src, nullptr, ld, q, s, (cudaStream_t)stream);
+}
+
+moe_status moe_ckpt8_unpack(int32_t dtype, int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* s,
+                            void* dst, int64_t ld, void* stream) {
+  TRY(check_ckpt8(dtype, rows, cols, dst, &ld, q, s, "dst"));
+  const Device* dv;
+  TRY(device(&dv));
+  return ckpt8(*dv, false, dtype, rows, cols, nullptr, dst, ld, const_cast<uint8_t*>(q), const_cast<uint8_t*>(s),
+               (cudaStream_t)stream);
+}
+
+}  // extern "C"
