@@ -39,9 +39,11 @@ MOE_DEV uint4 pack16x8(int f16, const float* v) {
 }
 
 // --- activations -----------------------------------------------------------------
+// The hardware exponential and quotient are within 2^-20 of |z| (or of 1 for a
+// slope), far below half a step of the 16-bit outputs.
 MOE_DEV float fn_value(int fn, float z) {
   switch (fn) {
-    case MOE_FN_SILU: return z / (1.0f + expf(-z));
+    case MOE_FN_SILU: return __fdividef(z, 1.0f + __expf(-z));
     case MOE_FN_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
     case MOE_FN_RELU: return z < 0.0f ? 0.0f : z;      // keeps NaN
     default: return z;
@@ -51,7 +53,7 @@ MOE_DEV float fn_value(int fn, float z) {
 MOE_DEV void fn_slope(int fn, float z, float& f, float& d) {
   switch (fn) {
     case MOE_FN_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z));
+      const float s = __fdividef(1.0f, 1.0f + __expf(-z));
       f = z * s;
       d = s * (1.0f + z * (1.0f - s));
       return;
@@ -59,7 +61,7 @@ MOE_DEV void fn_slope(int fn, float z, float& f, float& d) {
     case MOE_FN_GELU: {
       const float p = 0.5f * (1.0f + erff(z * 0.70710678f));
       f = z * p;
-      d = p + z * (0.39894228f * expf(-0.5f * z * z));
+      d = p + z * (0.39894228f * __expf(-0.5f * z * z));
       return;
     }
     case MOE_FN_RELU:
@@ -104,6 +106,55 @@ MOE_DEV void e4m3_unquad(uint32_t w, float scale, float* v) {
   v[1] = a.y * scale;
   v[2] = b.x * scale;
   v[3] = b.y * scale;
+}
+
+// --- epilogues on 8 neighbouring columns of one row -----------------------------------
+// bias, activation, residual, store (kEpiLinear); v is used up
+MOE_DEV void linear8(const DenseGemmArgs& a, int seg, int row, int c, float (&v)[8]) {
+  float t[8];
+  if (a.bias) {
+    unpack16x8(a.f16, ldg16(static_cast<const uint16_t*>(a.bias) + c), t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  if (a.pre)
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.pre) + (size_t)row * a.N + c) = pack16x8(a.f16, v);
+  if (a.fn) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fn_value(a.fn, v[i]);
+  }
+  if (a.residual) {
+    // not through the read-only path: y may be the residual itself
+    unpack16x8(a.f16, *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
+                                                      (size_t)row * a.ldr + c), t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+  }
+  const size_t o = (size_t)row * a.ldo + c;
+  if (a.out_f32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out[seg]) + o);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[seg]) + o) = pack16x8(a.f16, v);
+  }
+}
+// h = f(g) u, and g and u in 16 bits when they are saved so (kEpiGlu)
+MOE_DEV void glu8(const DenseGemmArgs& a, int row, int c, const float (&g)[8], const float (&u)[8]) {
+  float h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = fn_value(a.fn, g[i]) * u[i];
+  const size_t o = (size_t)row * a.N + c;
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[0]) + o) = pack16x8(a.f16, h);
+  if (a.g && !a.saved8) {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.g) + o) = pack16x8(a.f16, g);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.u) + o) = pack16x8(a.f16, u);
+  }
+}
+// 8 of a block's codes, its inverse scale given
+MOE_DEV void codes8(const DenseGemmArgs& a, void* q, int row, int c, const float (&v)[8], float inv) {
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q) + (size_t)row * a.N + c) =
+      make_uint2(e4m3_quad(v, inv), e4m3_quad(v + 4, inv));
 }
 
 namespace tc {
@@ -189,19 +240,49 @@ MOE_DEV void tma_load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, u
 MOE_DEV void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// wait_or_abort for a barrier that threads of another CTA arrive on
-MOE_DEV bool wait_or_abort_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                   uint32_t limit = 1u << 22) {
+// One lane of the warp, by elect.sync: the compiler then knows that the branch
+// holds one thread, so the tcgen05 and TMA instructions in it take their
+// operands from uniform registers. Behind `lane == 0` each was wrapped in a
+// loop over the active lanes: a stage of four 256x256x16 MMAs cost 0.42 us,
+// with elect.sync 0.37 us (256x128: 0.39 and 0.30).
+MOE_DEV bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+MOE_DEV uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;\n" : "=l"(t));
+  return t;
+}
+// Bounded wait on phase `parity` of `bar` that gives up after about `limit_ns`
+// or as soon as another role of the CTA has raised `*abort` (raising it
+// itself on a timeout). kCluster: threads of another CTA arrive on `bar`.
+template <bool kCluster = false>
+MOE_DEV bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
+                          uint64_t limit_ns = 4000000000ull) {
   const uint32_t a = smem_u32(bar);
-  for (uint32_t it = 0; it < limit; ++it) {
+  uint64_t t0 = 0;
+  while (true) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done) : "r"(a), "r"(parity), "r"(1000u) : "memory");
+    if constexpr (kCluster)
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(a), "r"(parity) : "memory");
+    else
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(a), "r"(parity) : "memory");
     if (done) return true;
     if (*abort) return false;
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > limit_ns) break;
   }
   *abort = 1;
   return false;

@@ -47,8 +47,27 @@ struct DenseGemmArgs {
 
 template <int kEpi, bool kAMn, bool kBMn, int kCg>
 __global__ void k_dense_gemm(const __grid_constant__ DenseGemmArgs a);
-size_t dense_gemm_smem_bytes(int cg);
+size_t dense_gemm_smem_bytes();
 int dense_gemm_threads();
+
+// --- few tokens (dense_rows.cu) -------------------------------------------------
+// The weights are the MMA's 128 rows (map_a; kEpiGlu: 64 gate and 64 up rows),
+// the tokens its columns (map_b[0], tile_n = T rounded up to 16). A cluster of
+// `splits` CTAs divides K and adds its partial sums through shared memory.
+// M, N, K as above (M tokens, N outputs); early: the weights are not written
+// by the previous kernel of the stream and may be loaded before it ends.
+struct DenseRowsArgs {
+  DenseGemmArgs g;
+  int splits, stages, early;
+};
+constexpr int kRowsTokens = 64;         // most tokens of this kernel
+constexpr int kRowsThreads = 192;
+constexpr int kRowsRing = 110 * 1024;   // two CTAs of an SM, so the next call starts under this one
+template <int kEpi>
+__global__ void k_dense_rows(const __grid_constant__ DenseRowsArgs a);
+constexpr int dense_rows_stage(int tile_n) { return 128 * 128 + tile_n * 128; }
+constexpr int dense_rows_max_stages() { return kRowsRing / dense_rows_stage(16); }
+constexpr size_t dense_rows_smem_bytes() { return kRowsRing + 1024; }
 
 // --- element kernels (dense_elem.cu) ------------------------------------------
 // dz = dy * f'(pre) rounded to 16 bits (dz NULL: not written; pre NULL: f' = 1)

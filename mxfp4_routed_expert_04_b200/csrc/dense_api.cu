@@ -153,10 +153,14 @@ struct Device {
 std::mutex g_mu;
 Device g_dev[64];
 
-template <int kEpi, bool kAMn, bool kBMn, int kCg>
+template <int kEpi, bool kAMn, bool kBMn>
 cudaError_t allow_smem() {
-  return cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, kAMn, kBMn, kCg>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)moe::dense_gemm_smem_bytes(kCg));
+  const int bytes = (int)moe::dense_gemm_smem_bytes();
+  const cudaError_t e = cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, kAMn, kBMn, 1>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e != cudaSuccess ? e
+                          : cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, kAMn, kBMn, 2>,
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 moe_status device(const Device** out) {
@@ -167,11 +171,17 @@ moe_status device(const Device** out) {
   Device& s = g_dev[dev];
   if (!s.ready) {
     cudaError_t e = cudaDeviceGetAttribute(&s.num_sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, false, 1>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, true, 1>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, true, true, 1>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu, false, false, 1>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu, false, true, 1>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, false>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, true>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, true, true>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu, false, false>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu, false, true>();
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(moe::k_dense_rows<moe::kEpiLinear>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)moe::dense_rows_smem_bytes());
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(moe::k_dense_rows<moe::kEpiGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)moe::dense_rows_smem_bytes());
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "device setup: %s", cudaGetErrorString(e));
     s.ready = true;
   }
@@ -240,21 +250,71 @@ struct Mat {
   int64_t rows, cols, ld;
 };
 
+// Tile of a product: a pair's 256 rows or one CTA's 128, and the columns, from
+// the time of a wave of tiles in a long product. That time grows with the
+// columns (MMAs) and with a constant (the A rows every tile loads): measured at
+// 4096 x 4096 x 8192, pairs of 256 / 192 / 160 / 128 columns 188 / 189 / 197 /
+// 213 us, single CTAs of 256 / 192 / 128 columns 218 / 223 / 257 us, which the
+// two lines below fit within 5%. MN-major B comes in boxes of 64 columns per CTA.
+struct TileChoice {
+  int cg, n;
+};
+TileChoice pick_tile(const Device& dv, int M, int m_segs, long N, bool glu, bool b_mn) {
+  TileChoice best = {1, 64};
+  long best_cost = -1;
+  for (int cg = M > 128 ? 2 : 1; cg >= 1; --cg) {
+    for (int n = 256; n >= 64; n -= 32) {
+      if (b_mn && n % (64 * cg) != 0) continue;
+      if (glu && n % 64 != 0) continue;
+      const long cols = glu ? n / 2 : n;
+      const long tiles = m_segs * (long)((M + 128 * cg - 1) / (128 * cg)) * ((N + cols - 1) / cols);
+      const long slots = dv.num_sms / cg, waves = (tiles + slots - 1) / slots;
+      const long cost = waves * (cg == 2 ? 100L * (n + 100) : 107L * (n + 136));
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best = {cg, n};
+      }
+    }
+  }
+  return best;
+}
+
 template <int kEpi, bool kAMn, bool kBMn>
-moe_status gemm(const Device& dv, moe::DenseGemmArgs& g, const Mat* a, int na, const Mat* b, int nb, int tile_n,
+moe_status gemm(const Device& dv, moe::DenseGemmArgs& g, const Mat* a, int na, const Mat* b, int nb,
                 cudaStream_t st, const char* what) {
-  constexpr int cg = 1;
-  g.tile_n = tile_n;
+  constexpr bool glu = kEpi == moe::kEpiGlu;
+  const TileChoice t = pick_tile(dv, g.M, g.m_segs, g.N, glu, kBMn);
+  g.tile_n = t.n;
   for (int i = 0; i < na; ++i)
     TRY(map16(&g.map_a[i], a[i].p, g.f16, a[i].rows, a[i].cols, a[i].ld, kAMn ? 64 : 128, what));
   for (int i = 0; i < nb; ++i)
     TRY(map16(&g.map_b[i], b[i].p, g.f16, b[i].rows, b[i].cols, b[i].ld,
-              kBMn ? 64 : kEpi == moe::kEpiGlu ? tile_n / 2 : tile_n / cg, what));
-  const int cols = kEpi == moe::kEpiGlu ? tile_n / 2 : tile_n;
-  const long tiles = (long)g.m_segs * ((g.M + 128 * cg - 1) / (128 * cg)) * ((g.N + cols - 1) / cols);
-  const int ctas = (int)std::min<long>(tiles, dv.num_sms / cg) * cg;
-  return launch(what, moe::k_dense_gemm<kEpi, kAMn, kBMn, cg>, dim3((unsigned)ctas), moe::dense_gemm_threads(),
-                moe::dense_gemm_smem_bytes(cg), cg, st, g);
+              kBMn ? 64 : glu ? t.n / 2 : t.n / t.cg, what));
+  const int cols = glu ? t.n / 2 : t.n, rows = 128 * t.cg;
+  const long tiles = (long)g.m_segs * ((g.M + rows - 1) / rows) * ((g.N + cols - 1) / cols);
+  const int ctas = (int)std::min<long>(tiles, dv.num_sms / t.cg) * t.cg;
+  return launch(what, t.cg == 2 ? moe::k_dense_gemm<kEpi, kAMn, kBMn, 2> : moe::k_dense_gemm<kEpi, kAMn, kBMn, 1>,
+                dim3((unsigned)ctas), moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), t.cg, st, g);
+}
+
+// Few tokens: the weights' rows over clusters that split K, so that up to two
+// CTAs of every SM stream (each at least four stages of 64 k).
+template <int kEpi>
+moe_status rows(const Device& dv, const moe::DenseGemmArgs& g, const Mat& x, const Mat* w, bool early,
+                cudaStream_t st, const char* what) {
+  constexpr bool glu = kEpi == moe::kEpiGlu;
+  moe::DenseRowsArgs r;
+  r.g = g;
+  r.g.tile_n = (g.M + 15) / 16 * 16;
+  r.early = early;
+  TRY(map16(&r.g.map_b[0], x.p, g.f16, x.rows, x.cols, x.ld, r.g.tile_n, what));
+  for (int i = 0; i < (glu ? 2 : 1); ++i)
+    TRY(map16(&r.g.map_a[i], w[i].p, g.f16, w[i].rows, w[i].cols, w[i].ld, glu ? 64 : 128, what));
+  const int tile = glu ? 64 : 128, tiles = (g.N + tile - 1) / tile, ks = (g.K + 63) / 64;
+  r.splits = std::max(1, std::min(std::min(8, 2 * dv.num_sms / tiles), ks / 4));
+  r.stages = moe::kRowsRing / moe::dense_rows_stage(r.g.tile_n);
+  return launch(what, moe::k_dense_rows<kEpi>, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads,
+                moe::dense_rows_smem_bytes(), r.splits, st, r);
 }
 
 moe::DenseGemmArgs gemm_args(int M, int N, int K, int f16, void* ws) {
@@ -266,17 +326,16 @@ moe::DenseGemmArgs gemm_args(int M, int N, int K, int f16, void* ws) {
   return g;
 }
 
-int pick_tile_n(int N) { return N > 128 ? 256 : N > 64 ? 128 : 64; }
-
 // y[T, N] = f(x W^T + bias) + residual
 moe_status project(const Device& dv, int T, int N, int K, int f16, int fn, int out_f32, const void* x, int64_t ldx,
                    const void* w, const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
-                   void* pre, void* ws, cudaStream_t st, const char* what) {
+                   void* pre, void* ws, cudaStream_t st, const char* what, bool early = false) {
   moe::DenseGemmArgs g = gemm_args(T, N, K, f16, ws);
   g.fn = fn; g.out_f32 = out_f32; g.bias = bias; g.residual = residual; g.ldr = ldr;
   g.out[0] = y; g.ldo = ldy; g.pre = pre;
   const Mat a = {x, T, K, ldx}, b = {w, N, K, K};
-  return gemm<moe::kEpiLinear, false, false>(dv, g, &a, 1, &b, 1, pick_tile_n(N), st, what);
+  if (T <= moe::kRowsTokens) return rows<moe::kEpiLinear>(dv, g, a, &b, early, st, what);
+  return gemm<moe::kEpiLinear, false, false>(dv, g, &a, 1, &b, 1, st, what);
 }
 
 // dx[T, K] = sum_s dz_s[T, N] W_s[N, K]
@@ -284,7 +343,7 @@ moe_status input_grad(const Device& dv, int T, int N, int K, int f16, int out_f3
                       int segs, void* dx, int64_t lddx, void* ws, cudaStream_t st, const char* what) {
   moe::DenseGemmArgs g = gemm_args(T, K, N, f16, ws);
   g.k_segs = segs; g.out_f32 = out_f32; g.out[0] = dx; g.ldo = lddx;
-  return gemm<moe::kEpiLinear, false, true>(dv, g, dz, segs, w, segs, pick_tile_n(K), st, what);
+  return gemm<moe::kEpiLinear, false, true>(dv, g, dz, segs, w, segs, st, what);
 }
 
 // dw_s[N, K] = dz_s[T, N]^T x[T, K]
@@ -292,7 +351,7 @@ moe_status weight_grad(const Device& dv, int T, int N, int K, int f16, int out_f
                        const Mat& x, void* dw0, void* dw1, void* ws, cudaStream_t st, const char* what) {
   moe::DenseGemmArgs g = gemm_args(N, K, T, f16, ws);
   g.m_segs = segs; g.out_f32 = out_f32; g.out[0] = dw0; g.out[1] = dw1; g.ldo = K;
-  return gemm<moe::kEpiLinear, true, true>(dv, g, dz, segs, &x, 1, pick_tile_n(K), st, what);
+  return gemm<moe::kEpiLinear, true, true>(dv, g, dz, segs, &x, 1, st, what);
 }
 
 moe_status ckpt8(const Device& dv, bool pack, int f16, int64_t rows, int cols, const void* src, void* dst, int64_t ld,
@@ -456,11 +515,13 @@ moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, cons
   }
   const Mat xm = {x, p.T, p.H, p.ldx};
   const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}};
-  TRY((gemm<moe::kEpiGlu, false, false>(*dv, g, &xm, 1, wm, 2, p.I > 64 ? 256 : 128, st, "gate/up projection")));
+  const bool few = p.T <= moe::kRowsTokens;
+  TRY(few ? rows<moe::kEpiGlu>(*dv, g, xm, wm, false, st, "gate/up projection")
+          : (gemm<moe::kEpiGlu, false, false>(*dv, g, &xm, 1, wm, 2, st, "gate/up projection")));
   if (saved && saved->x_q)
     TRY(ckpt8(*dv, true, p.f16, p.T, p.H, x, nullptr, p.ldx, saved->x_q, saved->x_s, st));
   return project(*dv, p.T, p.H, p.I, p.f16, MOE_FN_NONE, p.out_f32, h, p.I, wd, nullptr, residual, p.ldr, y, p.ldy,
-                 nullptr, ws, st, "down projection");
+                 nullptr, ws, st, "down projection", true);
 }
 
 moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dy, const void* x, const void* wg,
@@ -500,7 +561,7 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dy, const void
   g.g = saved->g; g.u = saved->u; g.g_s = saved->g_s; g.u_s = saved->u_s;
   g.out[0] = at(ws, p.off_dg); g.out[1] = at(ws, p.off_du); g.pre = at(ws, p.off_h);
   const Mat wdm = {wd, p.H, p.I, p.I};
-  TRY((gemm<moe::kEpiDGlu, false, true>(*dv, g, &dym, 1, &wdm, 1, pick_tile_n(p.I), st, "hidden gradient")));
+  TRY((gemm<moe::kEpiDGlu, false, true>(*dv, g, &dym, 1, &wdm, 1, st, "hidden gradient")));
   const Mat dgu[2] = {{g.out[0], p.T, p.I, p.I}, {g.out[1], p.T, p.I, p.I}};
   if (dx) {
     const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}};

@@ -11,7 +11,12 @@
 // columns and k past a matrix read as zeros (the tensor maps' fill) and are
 // not stored.
 //
-// Roles: warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-5 run the
+// kCg = 2: a pair of CTAs (cluster) shares a tile of 256 rows. Each loads its
+// own 128 rows of A and half of B; the first CTA's MMAs read both halves of B
+// from both shared memories, so B crosses shared memory once per 256 rows and
+// the ring holds more k.
+//
+// Roles: warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-9 run the
 // epilogue out of one accumulator buffer while the next tile fills the other.
 // Every wait is bounded; a wait that gives up raises the CTA's abort flag and
 // the status word.
@@ -21,10 +26,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpiWarps = 8;                       // two per 32-row quarter of the accumulator
+constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxStages = 10;
 constexpr int kATile = 128 * 128;                  // 128 rows x 64 elements of 16 bits
-constexpr int kRing = 220 * 1024;
+constexpr int kRing = 225 * 1024;
 constexpr int kGroupM = 8;                         // row tiles that share their column tiles in L2
 
 struct Tile {
@@ -33,42 +39,16 @@ struct Tile {
 
 }  // namespace
 
-// the 32 accumulator columns at col of row `row`: bias, activation, residual, store
+// the 32 accumulator columns at col of row `row`
 MOE_DEV void epi_linear(const DenseGemmArgs& a, int seg, int row, int col, const uint32_t (&d)[32]) {
   if (row >= a.M) return;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = col + 8 * j;
-    if (c >= a.N) break;
-    float v[8], t[8];
+    if (col + 8 * j >= a.N) break;
+    float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(d[8 * j + i]);
-    if (a.bias) {
-      unpack16x8(a.f16, ldg16(static_cast<const uint16_t*>(a.bias) + c), t);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += t[i];
-    }
-    if (a.pre)
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.pre) + (size_t)row * a.N + c) = pack16x8(a.f16, v);
-    if (a.fn) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fn_value(a.fn, v[i]);
-    }
-    if (a.residual) {
-      // not through the read-only path: y may be the residual itself
-      unpack16x8(a.f16, *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
-                                                        (size_t)row * a.ldr + c), t);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += t[i];
-    }
-    const size_t o = (size_t)row * a.ldo + c;
-    if (a.out_f32) {
-      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out[seg]) + o);
-      p[0] = make_float4(v[0], v[1], v[2], v[3]);
-      p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[seg]) + o) = pack16x8(a.f16, v);
-    }
+    linear8(a, seg, row, col + 8 * j, v);
   }
 }
 
@@ -86,8 +66,7 @@ MOE_DEV void store_block8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, 
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(d[8 * j + i]);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q) + (size_t)row * a.N + col + 8 * j) =
-        make_uint2(e4m3_quad(v, inv), e4m3_quad(v + 4, inv));
+    codes8(a, q, row, col + 8 * j, v, inv);
   }
 }
 
@@ -99,21 +78,14 @@ MOE_DEV void epi_glu(const DenseGemmArgs& a, int row, int col, const uint32_t (&
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int c = col + 8 * j;
-    if (c >= a.N) break;
-    float gv[8], uv[8], h[8];
+    if (col + 8 * j >= a.N) break;
+    float gv[8], uv[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       gv[i] = __uint_as_float(g[8 * j + i]);
       uv[i] = __uint_as_float(u[8 * j + i]);
-      h[i] = fn_value(a.fn, gv[i]) * uv[i];
     }
-    const size_t o = (size_t)row * a.N + c;
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[0]) + o) = pack16x8(a.f16, h);
-    if (a.g && !a.saved8) {
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.g) + o) = pack16x8(a.f16, gv);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.u) + o) = pack16x8(a.f16, uv);
-    }
+    glu8(a, row, col + 8 * j, gv, uv);
   }
 }
 
@@ -181,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 4 * kCg);
+      mbar_init(&acc_empty[b], kEpiWarps * kCg);
     }
     mbar_init(&drain, 1);
     abort_flag = 0;
@@ -218,18 +190,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      uint32_t last_ph[kMaxStages];
-      bool filled[kMaxStages];
-#pragma unroll
-      for (int s = 0; s < kMaxStages; ++s) { last_ph[s] = 0; filled[s] = false; }
+    if (tc::elect_one()) {
       int s = 0;
       uint32_t ph = 0;
+      long issued = 0;
       bool ok = true;
       for (int q = first; q < tiles && ok; q += step) {
         const Tile t = tile_of(q);
         for (int j = 0; j < ks; ++j) {
-          if (!tc::wait_or_abort(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
+          if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
           uint8_t* sa = smem + s * stage_bytes;
           uint8_t* sb = sa + kATile;
           const int kseg = j >= ks1 ? 1 : 0;
@@ -259,20 +228,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
           } else {
             load(sb, mb, k0, t.n0 + (int)rank * bn);
           }
-          last_ph[s] = ph;
-          filled[s] = true;
+          ++issued;
           if (++s == nst) { s = 0; ph ^= 1u; }
         }
       }
-      if (*abort && rank == 0) {        // let every issued copy land before the CTA can exit
-        for (int s2 = 0; s2 < nst; ++s2)
-          if (filled[s2]) mbar_wait(&full[s2], last_ph[s2]);
+      // every stage handed back: no arrival of the pair's MMAs is left to come
+      for (int i = 0; i < nst && ok; ++i) {
+        ok = tc::wait_bounded(&empty[s], ph ^ 1u, abort);
+        if (++s == nst) { s = 0; ph ^= 1u; }
+      }
+      if (!ok && rank == 0) {           // let every issued copy land before the CTA can exit
+        for (int i = 0; i < nst && i < issued; ++i) {
+          const long last = (issued - 1 - i) / nst;           // last use of stage i
+          mbar_wait(&full[i], (uint32_t)(last & 1), 1u << 14);
+        }
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (rank == 0) {
+    // the whole loop in one elected thread
+    if (rank == 0 && tc::elect_one()) {
       const uint32_t idesc = tc::idesc_16(a.f16, 128 * kCg, tn, kAMn, kBMn);
       constexpr uint32_t a_step = kAMn ? 2048 >> 4 : 32 >> 4, b_step = kBMn ? 2048 >> 4 : 32 >> 4;
       int s = 0, n_it = 0;
@@ -281,60 +257,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
       for (int q = first; q < tiles && ok; q += step, ++n_it) {
         const int buf = n_it & 1;
         const uint32_t acc_ph = (uint32_t)((n_it >> 1) & 1);
-        if (!(kCg == 1 ? tc::wait_or_abort(&acc_empty[buf], acc_ph ^ 1u, abort)
-                       : tc::wait_or_abort_cluster(&acc_empty[buf], acc_ph ^ 1u, abort))) break;
+        if (!tc::wait_bounded<(kCg > 1)>(&acc_empty[buf], acc_ph ^ 1u, abort)) break;
         tc::fence_after_sync();
         const uint32_t d = tbase + 256u * buf;
         for (int j = 0; j < ks; ++j) {
-          if (!tc::wait_or_abort(&full[s], ph, abort)) { ok = false; break; }
-          tc::fence_after_sync();
-          if (lane == 0) {
-            const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kATile;
-            const uint64_t da = kAMn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa);
-            const uint64_t db = kBMn ? tc::desc_mn_sw128(sb, 8192) : tc::desc_sw128(sb);
+          if (!tc::wait_bounded(&full[s], ph, abort)) { ok = false; break; }
+          const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kATile;
+          const uint64_t da = kAMn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa);
+          const uint64_t db = kBMn ? tc::desc_mn_sw128(sb, 8192) : tc::desc_sw128(sb);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb)                    // K = 16 per MMA
-              tc::mma_16<kCg>(d, da + kb * a_step, db + kb * b_step, idesc, (j > 0 || kb > 0) ? 1u : 0u);
-            tc::commit_cg<kCg>(&empty[s]);
-            if (j == ks - 1) tc::commit_cg<kCg>(&acc_full[buf]);
-          }
-          __syncwarp();
+          for (int kb = 0; kb < 4; ++kb)                    // K = 16 per MMA
+            tc::mma_16<kCg>(d, da + kb * a_step, db + kb * b_step, idesc, (j > 0 || kb > 0) ? 1u : 0u);
+          tc::commit_cg<kCg>(&empty[s]);
+          if (j == ks - 1) tc::commit_cg<kCg>(&acc_full[buf]);
           if (++s == nst) { s = 0; ph ^= 1u; }
         }
       }
       if (*abort) {                     // no MMA may run past the CTA's exit
-        if (lane == 0) {
-          tc::commit_cg<kCg>(&drain);
-          mbar_wait(&drain, 0);
-        }
-        __syncwarp();
+        tc::commit_cg<kCg>(&drain);
+        mbar_wait(&drain, 0);
       }
     }
+    __syncwarp();
   } else {
-    // ---------------- epilogue (warps 2-5) ----------------
-    const int wq = warp & 3;
+    // ---------------- epilogue (warps 2-9) ----------------
+    // two warps share a quarter's 32 rows: 32-column chunks in turn
+    const int wq = warp & 3, cfirst = 32 * ((warp - 2) >> 2);
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
     int n_it = 0;
     for (int q = first; q < tiles; q += step, ++n_it) {
       const Tile t = tile_of(q);
       const int buf = n_it & 1;
-      if (!tc::wait_or_abort(&acc_full[buf], (uint32_t)((n_it >> 1) & 1), abort)) break;
+      const bool ok = tc::wait_bounded(&acc_full[buf], (uint32_t)((n_it >> 1) & 1), abort);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc::fence_after_sync();
       const uint32_t dcol = tbase + lane_off + 256u * buf;
       const int row = t.m0 + 32 * wq + lane;
-      for (int c0 = 0; c0 < cols; c0 += 32) {
+      auto release = [&]() {            // accumulators read: the MMA may reuse them
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) {
+          if (kCg == 1) tc::mbar_arrive(&acc_empty[buf]);
+          else tc::arrive_cluster(tc::mapa(&acc_empty[buf], 0));
+        }
+      };
+      if (cfirst >= cols) release();
+      for (int c0 = cfirst; c0 < cols; c0 += 64) {
         uint32_t d[32], u[32];
         tc::ld_32cols(dcol + c0, d);
         if (kEpi == kEpiGlu) tc::ld_32cols(dcol + cols + c0, u);
         tc::wait_ld();
-        if (c0 + 32 >= cols) {          // accumulators read: the MMA may reuse them
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            if (kCg == 1) tc::mbar_arrive(&acc_empty[buf]);
-            else tc::arrive_cluster(tc::mapa(&acc_empty[buf], 0));
-          }
-        }
+        if (c0 + 64 >= cols) release();
         if (kEpi == kEpiGlu) epi_glu(a, row, t.n0 + c0, d, u);
         else if (kEpi == kEpiDGlu) epi_dglu(a, row, t.n0 + c0, d);
         else epi_linear(a, t.seg, row, t.n0 + c0, d);
@@ -357,8 +330,13 @@ template __global__ void k_dense_gemm<kEpiLinear, false, true, 1>(const __grid_c
 template __global__ void k_dense_gemm<kEpiLinear, true, true, 1>(const __grid_constant__ DenseGemmArgs);
 template __global__ void k_dense_gemm<kEpiGlu, false, false, 1>(const __grid_constant__ DenseGemmArgs);
 template __global__ void k_dense_gemm<kEpiDGlu, false, true, 1>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiLinear, false, false, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiLinear, false, true, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiLinear, true, true, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiGlu, false, false, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiDGlu, false, true, 2>(const __grid_constant__ DenseGemmArgs);
 
-size_t dense_gemm_smem_bytes(int) { return kRing + 1024; }
+size_t dense_gemm_smem_bytes() { return kRing + 1024; }
 int dense_gemm_threads() { return kThreads; }
 
 }  // namespace moe
