@@ -356,31 +356,45 @@ def _bad(message):
     return MoeError(1, message)
 
 
-def _tensor(t, name, dtype, shape, ld=0):
+def _tensor(t, name, dtype, shape, ld=0, dev=None):
     """Pointer of a tensor after its checks: type, shape, rows packed (or of
     pitch ld), on the current device. The library itself sees pointers only."""
+    if dev is None:
+        dev = _device()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+            (t.is_contiguous() if not ld or ld == shape[-1] else _pitched(t, shape, ld)):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise _bad(f"{name} is {t.dtype}, not {dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise _bad(f"{name} has shape {tuple(t.shape)}, not {shape}")
-    if ld and ld != shape[-1]:
-        if (shape[-1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) != ld):
-            raise _bad(f"{name} has strides {t.stride()}, not ({ld}, 1)")
-    elif not t.is_contiguous():
-        raise _bad(f"{name} is not contiguous and its pitch in the dims is that of packed rows")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise _bad(f"{name} is on {t.device}, not on the current CUDA device")
-    return t.data_ptr()
+    raise _bad(f"{name} has strides {t.stride()}, not rows of pitch {ld or shape[-1]}")
 
 
-def _opt(t, name, dtype, shape, ld=0):
-    return None if t is None else _tensor(t, name, dtype, shape, ld)
+def _pitched(t, shape, ld):
+    return (shape[1] == 1 or t.stride(1) == 1) and (shape[0] == 1 or t.stride(0) == ld)
 
 
-def _ws_args(ws):
-    if ws.device.type != "cuda" or ws.device.index != torch.cuda.current_device() or not ws.is_contiguous():
+def _device():
+    """The current CUDA device (-2, which no tensor is on, without one)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
+def _opt(t, name, dtype, shape, ld=0, dev=None):
+    return None if t is None else _tensor(t, name, dtype, shape, ld, dev)
+
+
+def _ws_args(ws, dev=None):
+    if ws.get_device() != (_device() if dev is None else dev) or not ws.is_contiguous():
         raise _bad("the workspace is not a contiguous tensor on the current CUDA device")
-    return ws.data_ptr(), _nbytes(ws)
+    return ws.data_ptr(), ws.nbytes
+
+
+def _raw_stream(stream, dev):
+    """_stream() without building a Stream object for the current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _types(dims):
@@ -414,23 +428,25 @@ def moe_ffn_workspace_size(dims: MoeFfnDims) -> int:
 def moe_linear(dims, x, w, bias, residual, y, pre, ws, stream=None):
     """y = f(x W^T + bias) + residual; pre (or None) receives the argument of f."""
     t16, out = _types(dims)
-    T, N, K = dims.T, dims.N, dims.K
-    wp, wn = _ws_args(ws)
+    T, N, K, dev = dims.T, dims.N, dims.K, _device()
+    wp, wn = _ws_args(ws, dev)
     _check(_lib.moe_linear(
-        ctypes.byref(dims), _tensor(x, "x", t16, (T, K), dims.ldx), _tensor(w, "w", t16, (N, K)),
-        _opt(bias, "bias", t16, (N,)), _opt(residual, "residual", t16, (T, N), dims.ldr),
-        _tensor(y, "y", out, (T, N), dims.ldy), _opt(pre, "pre", t16, (T, N)), wp, wn, _stream(stream)))
+        dims, _tensor(x, "x", t16, (T, K), dims.ldx, dev), _tensor(w, "w", t16, (N, K), 0, dev),
+        _opt(bias, "bias", t16, (N,), 0, dev), _opt(residual, "residual", t16, (T, N), dims.ldr, dev),
+        _tensor(y, "y", out, (T, N), dims.ldy, dev), _opt(pre, "pre", t16, (T, N), 0, dev), wp, wn,
+        _raw_stream(stream, dev)))
 
 
 def moe_linear_backward(dims, dy, x, w, pre, dx, dw, dbias, ws, stream=None):
     """Gradients of moe_linear; dx, dw and dbias may each be None (not wanted)."""
     t16, out = _types(dims)
-    T, N, K = dims.T, dims.N, dims.K
-    wp, wn = _ws_args(ws)
+    T, N, K, dev = dims.T, dims.N, dims.K, _device()
+    wp, wn = _ws_args(ws, dev)
     _check(_lib.moe_linear_backward(
-        ctypes.byref(dims), _tensor(dy, "dy", t16, (T, N), dims.ldy), _opt(x, "x", t16, (T, K), dims.ldx),
-        _opt(w, "w", t16, (N, K)), _opt(pre, "pre", t16, (T, N)), _opt(dx, "dx", out, (T, K), dims.ldx),
-        _opt(dw, "dw", out, (N, K)), _opt(dbias, "dbias", out, (N,)), wp, wn, _stream(stream)))
+        dims, _tensor(dy, "dy", t16, (T, N), dims.ldy, dev), _opt(x, "x", t16, (T, K), dims.ldx, dev),
+        _opt(w, "w", t16, (N, K), 0, dev), _opt(pre, "pre", t16, (T, N), 0, dev),
+        _opt(dx, "dx", out, (T, K), dims.ldx, dev), _opt(dw, "dw", out, (N, K), 0, dev),
+        _opt(dbias, "dbias", out, (N,), 0, dev), wp, wn, _raw_stream(stream, dev)))
 
 
 class FfnSaved:
@@ -457,67 +473,69 @@ class FfnSaved:
         self.g = torch.empty(T, I, **kind) if g is None else g
         self.u = torch.empty(T, I, **kind) if u is None else u
 
-    def _ptrs(self, dims):
+    def _ptrs(self, dims, dev):
         T, H, I = dims.T, dims.H, dims.I
         t = torch.uint8 if dims.save == SAVE_8 else _types(dims)[0]
         ni, nh = (I + 31) // 32, (H + 31) // 32
         u8 = torch.uint8
         return _FfnSavedPtrs(
-            g=_tensor(self.g, "saved.g", t, (T, I)), u=_tensor(self.u, "saved.u", t, (T, I)),
-            g_s=_opt(self.g_s, "saved.g_s", u8, (T, ni)), u_s=_opt(self.u_s, "saved.u_s", u8, (T, ni)),
-            x_q=_opt(self.x_q, "saved.x_q", u8, (T, H)), x_s=_opt(self.x_s, "saved.x_s", u8, (T, nh)))
-
-
-def _saved(saved, dims):
-    return None if saved is None else ctypes.byref(saved._ptrs(dims))
+            _tensor(self.g, "saved.g", t, (T, I), 0, dev), _tensor(self.u, "saved.u", t, (T, I), 0, dev),
+            _opt(self.g_s, "saved.g_s", u8, (T, ni), 0, dev), _opt(self.u_s, "saved.u_s", u8, (T, ni), 0, dev),
+            _opt(self.x_q, "saved.x_q", u8, (T, H), 0, dev), _opt(self.x_s, "saved.x_s", u8, (T, nh), 0, dev))
 
 
 def moe_ffn(dims, x, wg, wu, wd, residual, y, saved, ws, stream=None):
     """y = (f(x Wg^T) * (x Wu^T)) Wd^T + residual; saved: an FfnSaved, or None with SAVE_NONE."""
     t16, out = _types(dims)
-    T, H, I = dims.T, dims.H, dims.I
-    wp, wn = _ws_args(ws)
+    T, H, I, dev = dims.T, dims.H, dims.I, _device()
+    wp, wn = _ws_args(ws, dev)
     _check(_lib.moe_ffn(
-        ctypes.byref(dims), _tensor(x, "x", t16, (T, H), dims.ldx), _tensor(wg, "wg", t16, (I, H)),
-        _tensor(wu, "wu", t16, (I, H)), _tensor(wd, "wd", t16, (H, I)),
-        _opt(residual, "residual", t16, (T, H), dims.ldr), _tensor(y, "y", out, (T, H), dims.ldy),
-        _saved(saved, dims), wp, wn, _stream(stream)))
+        dims, _tensor(x, "x", t16, (T, H), dims.ldx, dev), _tensor(wg, "wg", t16, (I, H), 0, dev),
+        _tensor(wu, "wu", t16, (I, H), 0, dev), _tensor(wd, "wd", t16, (H, I), 0, dev),
+        _opt(residual, "residual", t16, (T, H), dims.ldr, dev), _tensor(y, "y", out, (T, H), dims.ldy, dev),
+        None if saved is None else saved._ptrs(dims, dev), wp, wn, _raw_stream(stream, dev)))
 
 
 def moe_ffn_backward(dims, dy, x, wg, wu, wd, saved, dx, dwg, dwu, dwd, ws, stream=None):
     """Gradients of moe_ffn from `saved` (x None: from its 8-bit checkpoint);
     dx, dwd and the pair dwg, dwu may be None (not wanted)."""
     t16, out = _types(dims)
-    T, H, I = dims.T, dims.H, dims.I
-    wp, wn = _ws_args(ws)
+    T, H, I, dev = dims.T, dims.H, dims.I, _device()
+    wp, wn = _ws_args(ws, dev)
     _check(_lib.moe_ffn_backward(
-        ctypes.byref(dims), _tensor(dy, "dy", t16, (T, H), dims.ldy), _opt(x, "x", t16, (T, H), dims.ldx),
-        _opt(wg, "wg", t16, (I, H)), _opt(wu, "wu", t16, (I, H)), _tensor(wd, "wd", t16, (H, I)),
-        _saved(saved, dims), _opt(dx, "dx", out, (T, H), dims.ldx), _opt(dwg, "dwg", out, (I, H)),
-        _opt(dwu, "dwu", out, (I, H)), _opt(dwd, "dwd", out, (H, I)), wp, wn, _stream(stream)))
+        dims, _tensor(dy, "dy", t16, (T, H), dims.ldy, dev), _opt(x, "x", t16, (T, H), dims.ldx, dev),
+        _opt(wg, "wg", t16, (I, H), 0, dev), _opt(wu, "wu", t16, (I, H), 0, dev),
+        _tensor(wd, "wd", t16, (H, I), 0, dev), None if saved is None else saved._ptrs(dims, dev),
+        _opt(dx, "dx", out, (T, H), dims.ldx, dev), _opt(dwg, "dwg", out, (I, H), 0, dev),
+        _opt(dwu, "dwu", out, (I, H), 0, dev), _opt(dwd, "dwd", out, (H, I), 0, dev), wp, wn,
+        _raw_stream(stream, dev)))
 
 
-def _rows16(t, name):
+def _rows16(t, name, dev):
     if t.dim() != 2 or t.dtype not in _TORCH16:
         raise _bad(f"{name} is not a 2-D bf16 or f16 tensor")
     rows, cols = t.shape
     ld = t.stride(0) if rows > 1 else cols
-    return _TORCH16.index(t.dtype), rows, cols, ld, _tensor(t, name, t.dtype, (rows, cols), ld)
+    return _TORCH16.index(t.dtype), rows, cols, ld, _tensor(t, name, t.dtype, (rows, cols), ld, dev)
 
 
 def moe_ckpt8_pack(src, q, s, stream=None):
     """src [rows, cols] (bf16 or f16, any row pitch) -> E4M3 codes q [rows, cols]
     and E8M0 scales s [rows, ceil(cols / 32)], both uint8."""
-    dt, rows, cols, ld, p = _rows16(src, "src")
-    _check(_lib.moe_ckpt8_pack(dt, rows, cols, p, ld, _tensor(q, "q", torch.uint8, (rows, cols)),
-                               _tensor(s, "s", torch.uint8, (rows, (cols + 31) // 32)), _stream(stream)))
+    dev = _device()
+    dt, rows, cols, ld, p = _rows16(src, "src", dev)
+    _check(_lib.moe_ckpt8_pack(dt, rows, cols, p, ld, _tensor(q, "q", torch.uint8, (rows, cols), 0, dev),
+                               _tensor(s, "s", torch.uint8, (rows, (cols + 31) // 32), 0, dev),
+                               _raw_stream(stream, dev)))
 
 
 def moe_ckpt8_unpack(q, s, dst, stream=None):
     """The values an 8-bit checkpoint holds, into dst [rows, cols] (bf16 or f16)."""
-    dt, rows, cols, ld, p = _rows16(dst, "dst")
-    _check(_lib.moe_ckpt8_unpack(dt, rows, cols, _tensor(q, "q", torch.uint8, (rows, cols)),
-                                 _tensor(s, "s", torch.uint8, (rows, (cols + 31) // 32)), p, ld, _stream(stream)))
+    dev = _device()
+    dt, rows, cols, ld, p = _rows16(dst, "dst", dev)
+    _check(_lib.moe_ckpt8_unpack(dt, rows, cols, _tensor(q, "q", torch.uint8, (rows, cols), 0, dev),
+                                 _tensor(s, "s", torch.uint8, (rows, (cols + 31) // 32), 0, dev), p, ld,
+                                 _raw_stream(stream, dev)))
 
 
 class MoeFfn:

@@ -30,7 +30,7 @@ constexpr int kEpiWarps = 8;                       // two per 32-row quarter of 
 constexpr int kThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxStages = 10;
 constexpr int kATile = 128 * 128;                  // 128 rows x 64 elements of 16 bits
-constexpr int kRing = 225 * 1024;
+constexpr int kRing = 192 * 1024;
 constexpr int kGroupM = 8;                         // row tiles that share their column tiles in L2
 
 struct Tile {
@@ -39,94 +39,265 @@ struct Tile {
 
 }  // namespace
 
-// the 32 accumulator columns at col of row `row`
-MOE_DEV void epi_linear(const DenseGemmArgs& a, int seg, int row, int col, const uint32_t (&d)[32]) {
-  if (row >= a.M) return;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (col + 8 * j >= a.N) break;
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(d[8 * j + i]);
-    linear8(a, seg, row, col + 8 * j, v);
-  }
+// --- epilogue of one warp: 32 rows x 32 columns at a time ------------------------
+// A lane holds one row of the accumulator, but global rows are read and
+// written with neighbouring lanes on neighbouring 16 bytes (8 rows x 64 bytes
+// an instruction, whole sectors), and change hands in the warp's 4 KB of
+// shared memory: two buffers of 32 rows x 64 bytes, or one of 32 x 128. The
+// inputs of the next 32 columns are on their way while these are worked on
+// (with each lane on its own row and no look-ahead, 4096 x 8192 x 2048 with a
+// bias and a residual took 147 us, without them 106).
+struct EpiPos {
+  int row, col;             // first row and column of the 32 x 32 block
+};
+struct EpiIn {
+  uint4 a[4], b[4];         // kEpiLinear: residual, bias; kEpiDGlu: g, u
+  float sa, sb;             // kEpiDGlu: scales of this lane's row (8-bit)
+};
+
+// shared address of 16-byte chunk c of row r, rows of 64 (c < 4) or 128 (c < 8)
+// bytes: both ways round without bank conflicts
+MOE_DEV uint32_t stage64(uint32_t buf, int r, int c) { return buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4); }
+MOE_DEV uint32_t stage128(uint32_t buf, int r, int c) { return buf + r * 128 + ((c ^ (r & 7)) << 4); }
+// 8-byte chunk c of row r, rows of 32 bytes
+MOE_DEV uint32_t stage32(uint32_t buf, int r, int c) { return buf + r * 32 + ((c ^ ((r >> 2) & 3)) << 3); }
+MOE_DEV uint2 lds8b(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+MOE_DEV void sts8b(uint32_t addr, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(addr), "r"(v.x), "r"(v.y) : "memory");
 }
 
-// one row's 32 values as one block of an 8-bit checkpoint (columns past N are zeros)
-MOE_DEV void store_block8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, int col, const uint32_t (&d)[32]) {
+// this lane's pieces of the block's rows in global memory: row 8 i + lane / 4, columns 8 (lane % 4)..
+MOE_DEV bool piece(const DenseGemmArgs& a, const EpiPos& e, int i, int lane, int& r, int& c) {
+  r = e.row + 8 * i + (lane >> 2);
+  c = e.col + 8 * (lane & 3);
+  return r < a.M && c < a.N;
+}
+MOE_DEV void fetch16(const DenseGemmArgs& a, const EpiPos& e, const void* base, int64_t ld, int lane, uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int r, c;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (piece(a, e, i, lane, r, c))
+      v[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + (size_t)r * ld + c);
+  }
+}
+MOE_DEV void fetch8(const DenseGemmArgs& a, const EpiPos& e, const void* base, int lane, uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int r, c;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (piece(a, e, i, lane, r, c)) {
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + (size_t)r * a.N + c));
+      v[i].x = w.x;
+      v[i].y = w.y;
+    }
+  }
+}
+// pieces -> buffer
+MOE_DEV void pieces_to_stage(uint32_t buf, int lane, const uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sts16(stage64(buf, 8 * i + (lane >> 2), lane & 3), v[i]);
+}
+MOE_DEV void pieces8_to_stage(uint32_t buf, int lane, const uint4 (&v)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sts8b(stage32(buf, 8 * i + (lane >> 2), lane & 3), make_uint2(v[i].x, v[i].y));
+}
+// buffer (this lane's row in it, rounded to 16 bits) -> global rows
+MOE_DEV void row_to_stage(uint32_t buf, int lane, int f16, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sts16(stage64(buf, lane, j), pack16x8(f16, v + 8 * j));
+}
+MOE_DEV void flush16(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, void* base, int64_t ld) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int r, c;
+    if (piece(a, e, i, lane, r, c))
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + (size_t)r * ld + c) =
+          lds16(stage64(buf, 8 * i + (lane >> 2), lane & 3));
+  }
+}
+MOE_DEV void put16(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, const float (&v)[32], void* base,
+                   int64_t ld) {
+  __syncwarp();
+  row_to_stage(buf, lane, a.f16, v);
+  __syncwarp();
+  flush16(a, e, buf, lane, base, ld);
+}
+MOE_DEV void put32(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, const float (&v)[32], void* base,
+                   int64_t ld) {
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    sts16(stage128(buf, lane, j), make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                             __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = 4 * i + (lane >> 3), c = e.col + 4 * (lane & 7);
+    if (e.row + r < a.M && c < a.N)
+      *reinterpret_cast<uint4*>(static_cast<float*>(base) + (size_t)(e.row + r) * ld + c) =
+          lds16(stage128(buf, r, lane & 7));
+  }
+}
+// this lane's row as one block of an 8-bit checkpoint (columns past N are zeros)
+MOE_DEV void put8(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, const float (&v)[32], void* q,
+                  uint8_t* s) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = max(m, d[i] & 0x7FFFFFFFu);
+  for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   const uint32_t code = e4m3_scale_code(m);
   const float inv = e4m3_inv_scale(code);
-  s[(size_t)row * ((a.N + 31) / 32) + col / 32] = (uint8_t)code;
+  if (e.row + lane < a.M && e.col < a.N) s[(size_t)(e.row + lane) * ((a.N + 31) / 32) + e.col / 32] = (uint8_t)code;
+  __syncwarp();
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (col + 8 * j >= a.N) break;
-    float v[8];
+  for (int j = 0; j < 4; ++j)
+    sts8b(stage32(buf, lane, j), make_uint2(e4m3_quad(v + 8 * j, inv), e4m3_quad(v + 8 * j + 4, inv)));
+  __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(d[8 * j + i]);
-    codes8(a, q, row, col + 8 * j, v, inv);
+  for (int i = 0; i < 4; ++i) {
+    int r, c;
+    if (piece(a, e, i, lane, r, c))
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q) + (size_t)r * a.N + c) =
+          lds8b(stage32(buf, 8 * i + (lane >> 2), lane & 3));
   }
 }
 
-MOE_DEV void epi_glu(const DenseGemmArgs& a, int row, int col, const uint32_t (&g)[32], const uint32_t (&u)[32]) {
-  if (row >= a.M || col >= a.N) return;
-  if (a.g && a.saved8) {
-    store_block8(a, a.g, a.g_s, row, col, g);
-    store_block8(a, a.u, a.u_s, row, col, u);
-  }
+MOE_DEV void floats(const uint32_t (&d)[32], float (&v)[32]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (col + 8 * j >= a.N) break;
-    float gv[8], uv[8];
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(d[i]);
+}
+
+template <int kEpi>
+MOE_DEV void epi_fetch(const DenseGemmArgs& a, const EpiPos& e, int lane, EpiIn& in) {
+  if (kEpi == kEpiLinear) {
+    if (a.residual) fetch16(a, e, a.residual, a.ldr, lane, in.a);
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      gv[i] = __uint_as_float(g[8 * j + i]);
-      uv[i] = __uint_as_float(u[8 * j + i]);
+      for (int j = 0; j < 4; ++j)
+        in.b[j] = e.col + 8 * j < a.N ? ldg16(static_cast<const uint16_t*>(a.bias) + e.col + 8 * j)
+                                      : make_uint4(0u, 0u, 0u, 0u);
     }
-    glu8(a, row, col + 8 * j, gv, uv);
   }
-}
-
-MOE_DEV void epi_dglu(const DenseGemmArgs& a, int row, int col, const uint32_t (&d)[32]) {
-  if (row >= a.M || col >= a.N) return;
-  float gs = 1.0f, us = 1.0f;
-  if (a.saved8) {
-    const size_t so = (size_t)row * ((a.N + 31) / 32) + col / 32;
-    gs = e8m0_to_f32(a.g_s[so]);
-    us = e8m0_to_f32(a.u_s[so]);
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = col + 8 * j;
-    if (c >= a.N) break;
-    const size_t o = (size_t)row * a.N + c;
-    float gv[8], uv[8], dg[8], du[8], h[8];
+  if (kEpi == kEpiDGlu) {
     if (a.saved8) {
-      const uint2 gq = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.g) + o));
-      const uint2 uq = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.u) + o));
-      e4m3_unquad(gq.x, gs, gv);
-      e4m3_unquad(gq.y, gs, gv + 4);
-      e4m3_unquad(uq.x, us, uv);
-      e4m3_unquad(uq.y, us, uv + 4);
+      fetch8(a, e, a.g, lane, in.a);
+      fetch8(a, e, a.u, lane, in.b);
+      in.sa = in.sb = 0.0f;
+      if (e.row + lane < a.M && e.col < a.N) {
+        const size_t so = (size_t)(e.row + lane) * ((a.N + 31) / 32) + e.col / 32;
+        in.sa = e8m0_to_f32(__ldg(a.g_s + so));
+        in.sb = e8m0_to_f32(__ldg(a.u_s + so));
+      }
     } else {
-      unpack16x8(a.f16, ldg16(static_cast<const uint16_t*>(a.g) + o), gv);
-      unpack16x8(a.f16, ldg16(static_cast<const uint16_t*>(a.u) + o), uv);
+      fetch16(a, e, a.g, a.N, lane, in.a);
+      fetch16(a, e, a.u, a.N, lane, in.b);
+    }
+  }
+}
+
+MOE_DEV void epi_linear(const DenseGemmArgs& a, int seg, const EpiPos& e, uint32_t buf, int lane, const EpiIn& in,
+                        float (&v)[32]) {
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float t[8];
+      unpack16x8(a.f16, in.b[j], t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * j + i] += t[i];
+    }
+  }
+  if (a.pre) put16(a, e, buf, lane, v, a.pre, a.N);
+  if (a.fn) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = fn_value(a.fn, v[i]);
+  }
+  if (a.residual) {
+    __syncwarp();
+    pieces_to_stage(buf, lane, in.a);
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float t[8];
+      unpack16x8(a.f16, lds16(stage64(buf, lane, j)), t);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[8 * j + i] += t[i];
+    }
+  }
+  if (a.out_f32) put32(a, e, buf, lane, v, a.out[seg], a.ldo);
+  else put16(a, e, buf, lane, v, a.out[seg], a.ldo);
+}
+
+MOE_DEV void epi_glu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, float (&g)[32], float (&u)[32]) {
+  if (a.g) {
+    if (a.saved8) {
+      put8(a, e, buf, lane, g, a.g, a.g_s);
+      put8(a, e, buf + 2048, lane, u, a.u, a.u_s);
+    } else {
+      put16(a, e, buf, lane, g, a.g, a.N);
+      put16(a, e, buf + 2048, lane, u, a.u, a.N);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) g[i] = fn_value(a.fn, g[i]) * u[i];
+  put16(a, e, buf, lane, g, a.out[0], a.N);
+}
+
+MOE_DEV void epi_dglu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, const EpiIn& in,
+                      float (&dh)[32]) {
+  const uint32_t ga = buf, ua = buf + 2048;
+  __syncwarp();
+  if (a.saved8) {
+    pieces8_to_stage(ga, lane, in.a);
+    pieces8_to_stage(ua, lane, in.b);
+  } else {
+    pieces_to_stage(ga, lane, in.a);
+    pieces_to_stage(ua, lane, in.b);
+  }
+  __syncwarp();
+  uint4 gq[4], uq[4], hq[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float g[8], u[8], x[8], y[8], h[8];
+    if (a.saved8) {
+      const uint2 p = lds8b(stage32(ga, lane, j)), q = lds8b(stage32(ua, lane, j));
+      e4m3_unquad(p.x, in.sa, g);
+      e4m3_unquad(p.y, in.sa, g + 4);
+      e4m3_unquad(q.x, in.sb, u);
+      e4m3_unquad(q.y, in.sb, u + 4);
+    } else {
+      unpack16x8(a.f16, lds16(stage64(ga, lane, j)), g);
+      unpack16x8(a.f16, lds16(stage64(ua, lane, j)), u);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float dh = __uint_as_float(d[8 * j + i]);
       float f, s;
-      fn_slope(a.fn, gv[i], f, s);
-      dg[i] = dh * uv[i] * s;
-      du[i] = dh * f;
-      h[i] = f * uv[i];
+      fn_slope(a.fn, g[i], f, s);
+      x[i] = dh[8 * j + i] * u[i] * s;
+      y[i] = dh[8 * j + i] * f;
+      h[i] = f * u[i];
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[0]) + o) = pack16x8(a.f16, dg);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[1]) + o) = pack16x8(a.f16, du);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.pre) + o) = pack16x8(a.f16, h);
+    gq[j] = pack16x8(a.f16, x);
+    uq[j] = pack16x8(a.f16, y);
+    hq[j] = pack16x8(a.f16, h);
   }
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    sts16(stage64(ga, lane, j), gq[j]);
+    sts16(stage64(ua, lane, j), uq[j]);
+  }
+  __syncwarp();
+  flush16(a, e, ga, lane, a.out[0], a.N);
+  flush16(a, e, ua, lane, a.out[1], a.N);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sts16(stage64(ga, lane, j), hq[j]);
+  __syncwarp();
+  flush16(a, e, ga, lane, a.pre, a.N);
 }
 
 template <int kEpi, bool kAMn, bool kBMn, int kCg>
@@ -284,15 +455,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
     // two warps share a quarter's 32 rows: 32-column chunks in turn
     const int wq = warp & 3, cfirst = 32 * ((warp - 2) >> 2);
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
+    const uint32_t stage = smem_u32(smem + kRing) + 4096u * (uint32_t)(warp - 2);
     int n_it = 0;
     for (int q = first; q < tiles; q += step, ++n_it) {
       const Tile t = tile_of(q);
       const int buf = n_it & 1;
+      EpiPos e = {t.m0 + 32 * wq, t.n0 + cfirst};
+      EpiIn in;
+      if (cfirst < cols) epi_fetch<kEpi>(a, e, lane, in);
       const bool ok = tc::wait_bounded(&acc_full[buf], (uint32_t)((n_it >> 1) & 1), abort);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       tc::fence_after_sync();
       const uint32_t dcol = tbase + lane_off + 256u * buf;
-      const int row = t.m0 + 32 * wq + lane;
       auto release = [&]() {            // accumulators read: the MMA may reuse them
         tc::fence_before_sync();
         __syncwarp();
@@ -303,14 +477,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
       };
       if (cfirst >= cols) release();
       for (int c0 = cfirst; c0 < cols; c0 += 64) {
-        uint32_t d[32], u[32];
+        uint32_t d[32], d2[32];
         tc::ld_32cols(dcol + c0, d);
-        if (kEpi == kEpiGlu) tc::ld_32cols(dcol + cols + c0, u);
+        if (kEpi == kEpiGlu) tc::ld_32cols(dcol + cols + c0, d2);
+        const EpiIn now = in;
+        const EpiPos at = e;
+        if (kEpi != kEpiGlu && c0 + 64 < cols) {
+          e.col += 64;
+          epi_fetch<kEpi>(a, e, lane, in);
+        } else {
+          e.col += 64;
+        }
         tc::wait_ld();
         if (c0 + 64 >= cols) release();
-        if (kEpi == kEpiGlu) epi_glu(a, row, t.n0 + c0, d, u);
-        else if (kEpi == kEpiDGlu) epi_dglu(a, row, t.n0 + c0, d);
-        else epi_linear(a, t.seg, row, t.n0 + c0, d);
+        float v[32];
+        floats(d, v);
+        if (kEpi == kEpiGlu) {
+          float u[32];
+          floats(d2, u);
+          epi_glu(a, at, stage, lane, v, u);
+        } else if (kEpi == kEpiDGlu) {
+          epi_dglu(a, at, stage, lane, now, v);
+        } else {
+          epi_linear(a, t.seg, at, stage, lane, now, v);
+        }
       }
     }
   }
@@ -336,7 +526,7 @@ template __global__ void k_dense_gemm<kEpiLinear, true, true, 2>(const __grid_co
 template __global__ void k_dense_gemm<kEpiGlu, false, false, 2>(const __grid_constant__ DenseGemmArgs);
 template __global__ void k_dense_gemm<kEpiDGlu, false, true, 2>(const __grid_constant__ DenseGemmArgs);
 
-size_t dense_gemm_smem_bytes() { return kRing + 1024; }
+size_t dense_gemm_smem_bytes() { return kRing + 4096 * kEpiWarps + 1024; }
 int dense_gemm_threads() { return kThreads; }
 
 }  // namespace moe

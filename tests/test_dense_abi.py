@@ -165,10 +165,11 @@ def test_binding_checks_tensors():
         ptr(ok["x"].float())
     with pytest.raises(M.MoeError, match="shape"):
         ptr(ok["x"][:3])
-    with pytest.raises(M.MoeError, match="contiguous"):
-        ptr(torch.zeros(128, 4, dtype=torch.bfloat16).t())
+    on_dev = ok["x"].get_device()                # the layout checks, as if it were the current device
     with pytest.raises(M.MoeError, match="strides"):
-        ptr(ok["x"], ld=136)
+        M._tensor(torch.zeros(128, 4, dtype=torch.bfloat16).t(), "x", torch.bfloat16, (4, 128), 0, on_dev)
+    with pytest.raises(M.MoeError, match="strides"):
+        M._tensor(ok["x"], "x", torch.bfloat16, (4, 128), 136, on_dev)
     with pytest.raises(M.MoeError, match="not on the current CUDA device"):
         ptr(ok["x"])
     with pytest.raises(M.MoeError, match="workspace"):
