@@ -108,55 +108,6 @@ MOE_DEV void e4m3_unquad(uint32_t w, float scale, float* v) {
   v[3] = b.y * scale;
 }
 
-// --- epilogues on 8 neighbouring columns of one row -----------------------------------
-// bias, activation, residual, store (kEpiLinear); v is used up
-MOE_DEV void linear8(const DenseGemmArgs& a, int seg, int row, int c, float (&v)[8]) {
-  float t[8];
-  if (a.bias) {
-    unpack16x8(a.f16, ldg16(static_cast<const uint16_t*>(a.bias) + c), t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
-  if (a.pre)
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.pre) + (size_t)row * a.N + c) = pack16x8(a.f16, v);
-  if (a.fn) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = fn_value(a.fn, v[i]);
-  }
-  if (a.residual) {
-    // not through the read-only path: y may be the residual itself
-    unpack16x8(a.f16, *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.residual) +
-                                                      (size_t)row * a.ldr + c), t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
-  }
-  const size_t o = (size_t)row * a.ldo + c;
-  if (a.out_f32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out[seg]) + o);
-    p[0] = make_float4(v[0], v[1], v[2], v[3]);
-    p[1] = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[seg]) + o) = pack16x8(a.f16, v);
-  }
-}
-// h = f(g) u, and g and u in 16 bits when they are saved so (kEpiGlu)
-MOE_DEV void glu8(const DenseGemmArgs& a, int row, int c, const float (&g)[8], const float (&u)[8]) {
-  float h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = fn_value(a.fn, g[i]) * u[i];
-  const size_t o = (size_t)row * a.N + c;
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out[0]) + o) = pack16x8(a.f16, h);
-  if (a.g && !a.saved8) {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.g) + o) = pack16x8(a.f16, g);
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.u) + o) = pack16x8(a.f16, u);
-  }
-}
-// 8 of a block's codes, its inverse scale given
-MOE_DEV void codes8(const DenseGemmArgs& a, void* q, int row, int c, const float (&v)[8], float inv) {
-  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q) + (size_t)row * a.N + c) =
-      make_uint2(e4m3_quad(v, inv), e4m3_quad(v + 4, inv));
-}
-
 namespace tc {
 
 // kind::f16, fp32 accumulation; M rows over the CTAs of the group; a_mn / b_mn:

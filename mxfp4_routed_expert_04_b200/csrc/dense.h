@@ -59,15 +59,26 @@ int dense_gemm_threads();
 struct DenseRowsArgs {
   DenseGemmArgs g;
   int splits, stages, early;
+  const void* next;         // what the next kernel of the call streams, for L2 (16-byte aligned, or NULL)
+  uint64_t next_bytes;      // a multiple of 16
 };
+constexpr int kRowsSplits = 8;          // most CTAs of a cluster
 constexpr int kRowsTokens = 64;         // most tokens of this kernel
 constexpr int kRowsThreads = 192;
-constexpr int kRowsRing = 110 * 1024;   // two CTAs of an SM, so the next call starts under this one
+constexpr int kRowsMemory = 110 * 1024; // two CTAs of an SM, so the next call starts under this one
+constexpr int dense_rows_stage(int tile_n) { return 128 * 128 + tile_n * 128; }
+// The partial sums: 512 bytes a token, in units of 4 tokens and of 512 (gated:
+// 1024) bytes; pushed ones up to a unit more for each CTA of the cluster, behind
+// the ring; kept ones over it.
+constexpr int kRowsPush = 8;
+constexpr int dense_rows_stages(int T, int tile_n) {
+  return (kRowsMemory - (T > kRowsPush ? 0 : 512 * (T + 3) + 1024 * (kRowsSplits - 1))) / dense_rows_stage(tile_n);
+}
+static_assert(512 * kRowsTokens <= dense_rows_stage(16) * 2, "kept sums fit the ring's first two stages");
+constexpr int kDenseRowsStages = dense_rows_stages(16, 16);
+constexpr size_t dense_rows_smem_bytes() { return kRowsMemory + 1024; }
 template <int kEpi>
 __global__ void k_dense_rows(const __grid_constant__ DenseRowsArgs a);
-constexpr int dense_rows_stage(int tile_n) { return 128 * 128 + tile_n * 128; }
-constexpr int dense_rows_max_stages() { return kRowsRing / dense_rows_stage(16); }
-constexpr size_t dense_rows_smem_bytes() { return kRowsRing + 1024; }
 
 // --- element kernels (dense_elem.cu) ------------------------------------------
 // dz = dy * f'(pre) rounded to 16 bits (dz NULL: not written; pre NULL: f' = 1)

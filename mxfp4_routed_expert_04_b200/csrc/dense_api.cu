@@ -45,6 +45,7 @@ char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
   } while (0)
 
 constexpr size_t kStatusBytes = 256;
+constexpr uint64_t kPrefetchMax = 64u << 20;   // about half of the L2
 
 moe_status check_width(const char* name, int v) {
   if (v < 8 || v > 65536 || v % 8 != 0)
@@ -301,18 +302,20 @@ moe_status gemm(const Device& dv, moe::DenseGemmArgs& g, const Mat* a, int na, c
 // CTAs of every SM stream (each at least four stages of 64 k).
 template <int kEpi>
 moe_status rows(const Device& dv, const moe::DenseGemmArgs& g, const Mat& x, const Mat* w, bool early,
-                cudaStream_t st, const char* what) {
+                const Mat* next, cudaStream_t st, const char* what) {
   constexpr bool glu = kEpi == moe::kEpiGlu;
   moe::DenseRowsArgs r;
   r.g = g;
   r.g.tile_n = (g.M + 15) / 16 * 16;
   r.early = early;
+  r.next = next ? next->p : nullptr;
+  r.next_bytes = next ? std::min<uint64_t>((uint64_t)next->rows * next->cols * 2, kPrefetchMax) : 0;
   TRY(map16(&r.g.map_b[0], x.p, g.f16, x.rows, x.cols, x.ld, r.g.tile_n, what));
   for (int i = 0; i < (glu ? 2 : 1); ++i)
     TRY(map16(&r.g.map_a[i], w[i].p, g.f16, w[i].rows, w[i].cols, w[i].ld, glu ? 64 : 128, what));
   const int tile = glu ? 64 : 128, tiles = (g.N + tile - 1) / tile, ks = (g.K + 63) / 64;
-  r.splits = std::max(1, std::min(std::min(8, 2 * dv.num_sms / tiles), ks / 4));
-  r.stages = moe::kRowsRing / moe::dense_rows_stage(r.g.tile_n);
+  r.splits = std::max(1, std::min(std::min(moe::kRowsSplits, 7 * dv.num_sms / 4 / tiles), ks / 4));
+  r.stages = moe::dense_rows_stages(g.M, r.g.tile_n);
   return launch(what, moe::k_dense_rows<kEpi>, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads,
                 moe::dense_rows_smem_bytes(), r.splits, st, r);
 }
@@ -334,7 +337,7 @@ moe_status project(const Device& dv, int T, int N, int K, int f16, int fn, int o
   g.fn = fn; g.out_f32 = out_f32; g.bias = bias; g.residual = residual; g.ldr = ldr;
   g.out[0] = y; g.ldo = ldy; g.pre = pre;
   const Mat a = {x, T, K, ldx}, b = {w, N, K, K};
-  if (T <= moe::kRowsTokens) return rows<moe::kEpiLinear>(dv, g, a, &b, early, st, what);
+  if (T <= moe::kRowsTokens) return rows<moe::kEpiLinear>(dv, g, a, &b, early, nullptr, st, what);
   return gemm<moe::kEpiLinear, false, false>(dv, g, &a, 1, &b, 1, st, what);
 }
 
@@ -515,8 +518,9 @@ moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, cons
   }
   const Mat xm = {x, p.T, p.H, p.ldx};
   const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}};
+  const Mat wdm = {wd, p.H, p.I, p.I};
   const bool few = p.T <= moe::kRowsTokens;
-  TRY(few ? rows<moe::kEpiGlu>(*dv, g, xm, wm, false, st, "gate/up projection")
+  TRY(few ? rows<moe::kEpiGlu>(*dv, g, xm, wm, false, &wdm, st, "gate/up projection")
           : (gemm<moe::kEpiGlu, false, false>(*dv, g, &xm, 1, wm, 2, st, "gate/up projection")));
   if (saved && saved->x_q)
     TRY(ckpt8(*dv, true, p.f16, p.T, p.H, x, nullptr, p.ldx, saved->x_q, saved->x_s, st));

@@ -3,51 +3,156 @@
 //
 // A tile is 128 weight rows (the gated block: 64 gate and the same 64 up
 // rows) and all tokens, on tcgen05 with the weights as the M side. The CTAs of
-// a cluster each take a part of K, so that few rows still occupy every SM;
-// each leaves its fp32 sums in its own shared memory, and after a cluster
-// barrier every CTA adds its share of the outputs over the cluster's memories
-// in rank order (the same bits every run) and finishes them. Two CTAs fit an
-// SM: a following call's barriers, tensor memory and, where it may (`early`),
-// first weights are there before this one ends.
+// a cluster each take a part of K, so that few rows still occupy every SM.
+// Their fp32 sums are added in rank order (the same bits every run), in one of
+// two ways. Up to kRowsPush tokens every CTA writes its sums into the shared
+// memory of the CTA that finishes the outputs, and one cluster barrier later
+// they are there. The remote stores of more tokens take longer than the round
+// trip they save: there each CTA keeps its sums, over its ring, and each
+// fetches its share of the outputs from all (one token of 7168 -> 2048: 6.6 us
+// pushed, 7.9 fetched; 16 tokens of 2048 -> 7168: 10.0 and 8.8). Two CTAs fit
+// an SM: a following call's barriers, tensor memory and, where it may
+// (`early`), first weights are there before this one ends.
 #include "dense.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int kRowsMaxStages = dense_rows_max_stages();
+constexpr int kPrefetch = 16384;        // bytes of one L2 prefetch
 
-MOE_DEV float4 ld_cluster(uint32_t addr) {
+MOE_DEV void st_cluster4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};\n"
+               ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+MOE_DEV float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
-
-// sum over the cluster, in rank order, of 8 floats at byte offset `off` of `base`
-MOE_DEV void cluster_sum8(const float* base, uint32_t off, int splits, float (&v)[8]) {
+MOE_DEV void add_parts(const float4 (&q)[kRowsSplits], int splits, float (&v)[4]) {
+  v[0] = q[0].x; v[1] = q[0].y; v[2] = q[0].z; v[3] = q[0].w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  for (int r = 0; r < splits; ++r) {
-    const uint32_t p = tc::mapa(base, (uint32_t)r) + off;
-    const float4 a = ld_cluster(p), b = ld_cluster(p + 16);
-    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  for (int r = 1; r < kRowsSplits; ++r) {
+    if (r < splits) {
+      v[0] += q[r].x; v[1] += q[r].y; v[2] += q[r].z; v[3] += q[r].w;
+    }
   }
 }
-
-// one 8-bit block of 32 columns held by four neighbouring lanes, 8 columns each
-MOE_DEV void store_part8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, int c, const float (&v)[8], bool on) {
-  uint32_t m = 0;
+// sum in rank order, all loads first: of pushed parts `stride` float4 apart
+MOE_DEV void sum_pushed(const float4* p, int splits, int stride, float (&v)[4]) {
+  float4 q[kRowsSplits];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  if (!on) m = 0;
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  for (int r = 0; r < kRowsSplits; ++r)
+    if (r < splits) q[r] = p[r * stride];
+  add_parts(q, splits, v);
+}
+// and of kept parts, at byte offset `off` of every CTA's `base`
+MOE_DEV void sum_kept(const float* base, uint32_t off, int splits, float (&v)[4]) {
+  float4 q[kRowsSplits];
+#pragma unroll
+  for (int r = 0; r < kRowsSplits; ++r)
+    if (r < splits) q[r] = ld_cluster4(tc::mapa(base, (uint32_t)r) + off);
+  add_parts(q, splits, v);
+}
+MOE_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory"); }
+MOE_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory"); }
+
+MOE_DEV float load16(int f16, const void* base, size_t off) {
+  const uint32_t w = static_cast<const uint16_t*>(base)[off];
+  float a, b;
+  unpack16(f16, w, a, b);
+  return a;
+}
+MOE_DEV void store16(void* base, size_t off, int f16, float v) {
+  static_cast<uint16_t*>(base)[off] = (uint16_t)(pack16(f16, v, v) & 0xFFFFu);
+}
+
+// a block of an 8-bit checkpoint, one column a lane (zero past N)
+MOE_DEV void store_lanes8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, int c, float v, bool on, int lane) {
+  const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
   const uint32_t code = e4m3_scale_code(m);
   if (!on) return;
-  codes8(a, q, row, c, v, e4m3_inv_scale(code));
+  static_cast<uint8_t*>(q)[(size_t)row * a.N + c] = (uint8_t)(e4m3_pair(v * e4m3_inv_scale(code), 0.0f) & 0xFFu);
+  if (lane == 0) s[(size_t)row * ((a.N + 31) / 32) + c / 32] = (uint8_t)code;
+}
+// one held by eight neighbouring lanes, 4 columns each
+MOE_DEV void store_quads8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, int c, const float (&v)[4], bool on) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  if (!on) m = 0;
+#pragma unroll
+  for (int x = 1; x < 8; x <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+  const uint32_t code = e4m3_scale_code(m);
+  if (!on) return;
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(q) + (size_t)row * a.N + c) = e4m3_quad(v, e4m3_inv_scale(code));
   if (c % 32 == 0) s[(size_t)row * ((a.N + 31) / 32) + c / 32] = (uint8_t)code;
+}
+MOE_DEV uint2 load4(const void* base, size_t off) {
+  return *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + off);
+}
+MOE_DEV void store4(void* base, size_t off, int f16, const float (&v)[4]) {
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + off) =
+      make_uint2(pack16(f16, v[0], v[1]), pack16(f16, v[2], v[3]));
+}
+MOE_DEV void add4(int f16, uint2 w, float (&v)[4]) {
+  float t[4];
+  unpack16(f16, w.x, t[0], t[1]);
+  unpack16(f16, w.y, t[2], t[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] += t[i];
+}
+
+// Kept sums: groups of 4 outputs, token by token, this CTA's share of the
+// cluster's in whole warps, so eight lanes hold a 32-column block.
+template <int kEpi>
+MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int rank, int S, int warp, int lane) {
+  constexpr int kPer = (kEpi == kEpiGlu ? 64 : 128) / 4;
+  const int groups = a.M * kPer;
+  for (int b = 32 * (rank * (kRowsThreads / 32) + warp); b < groups; b += S * kRowsThreads) {
+    const int i = b + lane, t = i / kPer, m = 4 * (i - t * kPer), c = n0 + m;
+    const bool on = i < groups && c < a.N;
+    const uint32_t off = on ? (uint32_t)((t * 128 + m) * 4) : 0u;
+    const size_t o = (size_t)t * a.N + c;
+    float v[4];
+    if (kEpi == kEpiGlu) {
+      float u[4];
+      sum_kept(part, off, S, v);
+      sum_kept(part, off + 256, S, u);          // the up rows, 64 further on
+      if (a.g && a.saved8) {
+        store_quads8(a, a.g, a.g_s, t, c, v, on);
+        store_quads8(a, a.u, a.u_s, t, c, u, on);
+      }
+      if (on) {
+        if (a.g && !a.saved8) {
+          store4(a.g, o, a.f16, v);
+          store4(a.u, o, a.f16, u);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = fn_value(a.fn, v[k]) * u[k];
+        store4(a.out[0], o, a.f16, v);
+      }
+    } else {
+      uint2 bias = make_uint2(0u, 0u), res = bias;
+      if (on && a.bias) bias = load4(a.bias, (size_t)c);
+      if (on && a.residual) res = load4(a.residual, (size_t)t * a.ldr + c);
+      sum_kept(part, off, S, v);
+      if (on) {
+        if (a.bias) add4(a.f16, bias, v);
+        if (a.pre) store4(a.pre, o, a.f16, v);
+        if (a.fn) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = fn_value(a.fn, v[k]);
+        }
+        if (a.residual) add4(a.f16, res, v);
+        const size_t y = (size_t)t * a.ldo + c;
+        if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.out[0]) + y) = make_float4(v[0], v[1], v[2], v[3]);
+        else store4(a.out[0], y, a.f16, v);
+      }
+    }
+  }
 }
 
 }  // namespace
@@ -58,11 +163,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t full[kRowsMaxStages], empty[kRowsMaxStages], acc_full;
+  __shared__ uint64_t full[kDenseRowsStages], empty[kDenseRowsStages], acc_full;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   volatile int* abort = &abort_flag;
   constexpr int kRows = kEpi == kEpiGlu ? 64 : 128;         // outputs of a tile
+  constexpr int kPer = kRows / 32;                          // units of 4 tokens
+  constexpr int kUnit = kEpi == kEpiGlu ? 64 : 32;          // rows (of 4 tokens) of a unit's part: gate, up
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tn = a.tile_n, nst = p.stages;
   const int stage_bytes = dense_rows_stage(tn);
@@ -70,7 +177,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   const int n0 = (int)blockIdx.x / S * kRows;
   const int ks = (a.K + 63) / 64;
   const int j0 = (int)((long)ks * rank / S), j1 = (int)((long)ks * (rank + 1) / S);
-  const uint32_t tcols = tn <= 32 ? 32u : tn <= 64 ? 64u : 128u;
+  const uint32_t tcols = tn <= 32 ? 32u : 64u;
+  // pushed: units of 4 tokens x 32 rows, [unit slot][rank][kUnit] of 4 tokens of a
+  // row, behind the ring; kept: floats [token][128 rows], over it
+  const bool push = a.M <= kRowsPush;
+  float4* parts = reinterpret_cast<float4*>(smem + (push ? nst * stage_bytes : 0));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < nst; ++s) {
@@ -84,6 +195,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   if (warp == 1) tc::alloc_cg<1>(&tmem_slot, tcols);
   tc::fence_before_sync();
   __syncthreads();
+  cluster_arrive();                     // this CTA runs: its memory may be written
   tc::fence_after_sync();
   const uint32_t tbase = tmem_slot;
 
@@ -117,6 +229,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
         load_x(s, j);
         if (++s == nst) { s = 0; ph ^= 1u; }
       }
+      // its loads are all on their way: this CTA's share of what the next kernel
+      // of the stream reads goes to L2 meanwhile
+      if (ok && p.next_bytes) {
+        const uint64_t per_cta = (p.next_bytes + gridDim.x - 1) / gridDim.x;
+        const uint64_t per16 = (per_cta + 15) / 16 * 16;
+        const uint64_t lo = per16 * blockIdx.x, hi = min(lo + per16, p.next_bytes);
+        for (uint64_t o = lo; o < hi; o += kPrefetch)
+          tc::prefetch_l2(static_cast<const uint8_t*>(p.next) + o, (uint32_t)min((uint64_t)kPrefetch, hi - o));
+      }
       if (!ok) {                        // let every issued copy land before the CTA can exit
         for (int i = 0; i < nst; ++i) mbar_wait(&full[i], i < s ? ph : ph ^ 1u, 1u << 14);
       }
@@ -148,48 +269,95 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
     pdl_wait();
   }
   pdl_trigger();
-  // every thread: the sums are complete, the ring's last loads and MMAs are done
-  tc::wait_bounded(&acc_full, 0, abort);
-  tc::fence_after_sync();
-  __syncthreads();
-  float* part = reinterpret_cast<float*>(smem);             // [tn][128], where the ring was
-  if (warp >= 2 && !*abort) {
-    const int wq = warp & 3;
-    for (int c0 = 0; c0 < tn; c0 += 16) {
-      uint32_t d[32];
-      tc::ld_16cols(tbase + ((uint32_t)(32 * wq) << 16) + c0, d);
-      tc::wait_ld();
+  cluster_wait();
+  if (warp >= 2) {
+    const int wq = warp & 3;            // which 32 of the 128 rows
+    const bool ok = tc::wait_bounded(&acc_full, 0, abort);
+    if (__all_sync(0xFFFFFFFFu, ok)) {  // the sums are complete
+      tc::fence_after_sync();
+      const uint32_t at = (uint32_t)(rank * kUnit + (kEpi == kEpiGlu ? 32 * (wq >> 1) : 0) + lane) * 16u;
+      int slot = 0, owner = wq & (kPer - 1);        // of unit kPer * (token / 4) + this warp's rows
+      for (int c0 = 0; c0 < a.M; c0 += 16) {
+        uint32_t d[32];
+        tc::ld_16cols(tbase + ((uint32_t)(32 * wq) << 16) + c0, d);
+        tc::wait_ld();
 #pragma unroll
-      for (int i = 0; i < 16; ++i) part[(c0 + i) * 128 + 32 * wq + lane] = __uint_as_float(d[i]);
-    }
-  }
-  tc::fence_before_sync();
-  if (S > 1) tc::cluster_sync();
-  else __syncthreads();
-  // groups of 8 outputs, token by token; this CTA's share of the cluster's in
-  // whole warps, so four lanes hold a 32-column block
-  const int per = kRows / 8, groups = a.M * per;
-  for (int b = 32 * (rank * (kRowsThreads / 32) + warp); b < groups; b += S * kRowsThreads) {
-    const int i = b + lane, t = i / per, m = 8 * (i - t * per);
-    const bool on = i < groups && n0 + m < a.N;
-    const int tt = min(t, a.M - 1);
-    float v[8];
-    cluster_sum8(part, (uint32_t)((tt * 128 + m) * 4), S, v);
-    if (kEpi == kEpiGlu) {
-      float u[8];
-      cluster_sum8(part, (uint32_t)((tt * 128 + 64 + m) * 4), S, u);
-      if (a.g && a.saved8) {
-        store_part8(a, a.g, a.g_s, t, n0 + m, v, on);
-        store_part8(a, a.u, a.u_s, t, n0 + m, u, on);
+        for (int i = 0; i < 16; i += 4) {
+          if (c0 + i < a.M) {
+            if (push) {
+              while (owner >= S) { owner -= S; ++slot; }
+              st_cluster4(tc::mapa(parts, (uint32_t)owner) + (uint32_t)(slot * S * kUnit * 16) + at, d + i);
+              owner += kPer;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                sts32(smem_u32(parts) + (uint32_t)(((c0 + i + k) * 128 + 32 * wq + lane) * 4), d[i + k]);
+            }
+          }
+        }
       }
-      if (on) glu8(a, t, n0 + m, v, u);
-    } else {
-      if (on) linear8(a, 0, t, n0 + m, v);
     }
   }
+  __syncwarp();
+  tc::fence_before_sync();
+  cluster_arrive();
+  // pushed: this CTA's units (unit u is CTA u % S's), one a warp and turn; the
+  // first one's inputs before the wait
+  const int units = push ? (a.M + 3) / 4 * kPer : 0;
+  const int first = rank + S * warp, step = S * (kRowsThreads / 32);
+  auto inputs = [&](int u, float& bias, float (&res)[4]) {
+    const int t = u / kPer * 4, c = n0 + 32 * (u % kPer) + lane;
+    const bool on = kEpi == kEpiLinear && u < units && c < a.N;
+    bias = on && a.bias ? load16(a.f16, a.bias, (size_t)c) : 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      res[k] = on && a.residual && t + k < a.M ? load16(a.f16, a.residual, (size_t)(t + k) * a.ldr + c) : 0.0f;
+  };
+  float bias, res[4];
+  inputs(first, bias, res);
+  cluster_wait();
+  if (!push) finish_kept<kEpi>(a, reinterpret_cast<const float*>(parts), n0, rank, S, warp, lane);
+  for (int u = first; u < units; u += step) {
+    const int t = u / kPer * 4, c = n0 + 32 * (u % kPer) + lane;
+    const float4* part = parts + (size_t)(u / S) * S * kUnit + lane;
+    float v[4], up[4];
+    sum_pushed(part, S, kUnit, v);
+    if (kEpi == kEpiGlu) sum_pushed(part + 32, S, kUnit, up);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (t + k >= a.M) break;                      // the same in every lane
+      const bool on = c < a.N;
+      const size_t o = (size_t)(t + k) * a.N + c;
+      if (kEpi == kEpiGlu) {
+        if (a.g && a.saved8) {
+          store_lanes8(a, a.g, a.g_s, t + k, c, v[k], on, lane);
+          store_lanes8(a, a.u, a.u_s, t + k, c, up[k], on, lane);
+        }
+        if (on) {
+          if (a.g && !a.saved8) {
+            store16(a.g, o, a.f16, v[k]);
+            store16(a.u, o, a.f16, up[k]);
+          }
+          store16(a.out[0], o, a.f16, fn_value(a.fn, v[k]) * up[k]);
+        }
+      } else {
+        const float z = v[k] + bias;
+        if (on && a.pre) store16(a.pre, o, a.f16, z);
+        const float y = fn_value(a.fn, z) + res[k];
+        if (on) {
+          if (a.out_f32) static_cast<float*>(a.out[0])[(size_t)(t + k) * a.ldo + c] = y;
+          else store16(a.out[0], (size_t)(t + k) * a.ldo + c, a.f16, y);
+        }
+      }
+    }
+    if (kEpi == kEpiLinear) inputs(u + step, bias, res);
+  }
+  __syncthreads();
   if (threadIdx.x == 0 && *abort) atomicOr(a.status, kStatusWaitTimeout);
-  if (S > 1) tc::cluster_sync();        // the other CTAs read this one's sums
-  else __syncthreads();
+  if (!push) {                          // the other CTAs fetch this one's sums
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tbase, tcols);
