@@ -41,36 +41,75 @@ MOE_DEV uint4 pack16x8(int f16, const float* v) {
 // --- activations -----------------------------------------------------------------
 // The hardware exponential and quotient are within 2^-20 of |z| (or of 1 for a
 // slope), far below half a step of the 16-bit outputs.
-MOE_DEV float fn_value(int fn, float z) {
-  switch (fn) {
-    case MOE_FN_SILU: return __fdividef(z, 1.0f + __expf(-z));
-    case MOE_FN_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    case MOE_FN_RELU: return z < 0.0f ? 0.0f : z;      // keeps NaN
-    default: return z;
+
+// The normal distribution function, 0.5 erfc(-z / sqrt 2), without a branch:
+// erfc(x) = t exp(-x^2 + P(t)) with t = 1 / (1 + x/2) for x >= 0, P a least-
+// squares fit of log(erfc(x) exp(x^2) / t) at Chebyshev nodes of t, within
+// 3e-7 of erfc in fp32 (and 1.1e-6 relative up to x = 3). erff, with its two
+// branches taken by neighbouring lanes, made the gated epilogue of one wave of
+// tiles cost more than its products.
+MOE_DEV float normal_cdf(float z) {
+  const float x = fabsf(z) * 0.70710678f;
+  const float t = __fdividef(1.0f, fmaf(0.5f, x, 1.0f));
+  float p = 0.16550989f;
+  p = fmaf(p, t, -0.79146308f);
+  p = fmaf(p, t, 1.4132031f);
+  p = fmaf(p, t, -1.0316575f);
+  p = fmaf(p, t, 0.19146229f);
+  p = fmaf(p, t, -0.13963148f);
+  p = fmaf(p, t, 0.081164606f);
+  p = fmaf(p, t, 0.3772234f);
+  p = fmaf(p, t, 0.99968636f);
+  p = fmaf(p, t, -1.2654976f);
+  const float half = 0.5f * t * __expf(fmaf(-x, x, p));
+  return z < 0.0f ? half : 1.0f - half;
+}
+MOE_DEV float silu_gate(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+MOE_DEV float relu_keep(float z) { return z < 0.0f ? 0.0f : z; }      // keeps NaN
+
+// v = f(v); the choice of f outside the loop, so that the elements overlap
+template <int n>
+MOE_DEV void fn_values(int fn, float (&v)[n]) {
+  if (fn == MOE_FN_SILU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));
+  } else if (fn == MOE_FN_GELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] *= normal_cdf(v[i]);
+  } else if (fn == MOE_FN_RELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] = relu_keep(v[i]);
   }
 }
-// f(z) and f'(z): silu s (1 + z (1 - s)), gelu Phi(z) + z phi(z), relu 1 for z > 0
-MOE_DEV void fn_slope(int fn, float z, float& f, float& d) {
-  switch (fn) {
-    case MOE_FN_SILU: {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-z));
-      f = z * s;
-      d = s * (1.0f + z * (1.0f - s));
-      return;
+// f = f(z) and s = f'(z): silu p (1 + z (1 - p)), gelu Phi(z) + z phi(z), relu 1 for z > 0
+template <int n>
+MOE_DEV void fn_slopes(int fn, const float (&z)[n], float (&f)[n], float (&s)[n]) {
+  if (fn == MOE_FN_SILU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float p = silu_gate(z[i]);
+      f[i] = z[i] * p;
+      s[i] = p * (1.0f + z[i] * (1.0f - p));
     }
-    case MOE_FN_GELU: {
-      const float p = 0.5f * (1.0f + erff(z * 0.70710678f));
-      f = z * p;
-      d = p + z * (0.39894228f * __expf(-0.5f * z * z));
-      return;
+  } else if (fn == MOE_FN_GELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float p = normal_cdf(z[i]);
+      f[i] = z[i] * p;
+      s[i] = p + z[i] * (0.39894228f * __expf(-0.5f * z[i] * z[i]));
     }
-    case MOE_FN_RELU:
-      f = z < 0.0f ? 0.0f : z;
-      d = z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-      return;
-    default:
-      f = z;
-      d = 1.0f;
+  } else if (fn == MOE_FN_RELU) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      f[i] = relu_keep(z[i]);
+      s[i] = z[i] > 0.0f ? 1.0f : (z[i] <= 0.0f ? 0.0f : z[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      f[i] = z[i];
+      s[i] = 1.0f;
+    }
   }
 }
 
@@ -212,6 +251,7 @@ MOE_DEV uint64_t global_ns() {
 // Bounded wait on phase `parity` of `bar` that gives up after about `limit_ns`
 // or as soon as another role of the CTA has raised `*abort` (raising it
 // itself on a timeout). kCluster: threads of another CTA arrive on `bar`.
+constexpr uint32_t kSuspendNs = 1000000;   // a waiting thread sleeps this long at most before it looks again
 template <bool kCluster = false>
 MOE_DEV bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
                           uint64_t limit_ns = 4000000000ull) {
@@ -222,13 +262,13 @@ MOE_DEV bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
     if constexpr (kCluster)
       asm volatile(
           "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(a), "r"(parity) : "memory");
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(a), "r"(parity), "r"(kSuspendNs) : "memory");
     else
       asm volatile(
           "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(a), "r"(parity) : "memory");
+          "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(a), "r"(parity), "r"(kSuspendNs) : "memory");
     if (done) return true;
     if (*abort) return false;
     const uint64_t t = global_ns();

@@ -21,46 +21,55 @@ enum DenseEpi {
   kEpiDGlu = 2,     // D = dh: dg = dh u f'(g), du = dh f(g), h = f(g) u
 };
 
-struct DenseGemmArgs {
+// One product. a_mn / b_mn: the operand's M / N dimension is contiguous in
+// memory, not its contraction dimension.
+struct DenseProblem {
   // A and B of the contraction segments (dX of the gated block: dG Wg + dU Wu),
   // or A of the row segments (dWg and dWu share B), or B of the gate and up halves
   CUtensorMap map_a[2], map_b[2];
+  void* out[2];             // kEpiLinear: per row segment; kEpiGlu: h; kEpiDGlu: dg, du
+  int64_t ldo;
   int M, N, K;              // rows of one row segment, output columns (h columns for kEpiGlu), contraction
   int k_segs;               // contraction segments (1 or 2)
   int m_segs;               // row segments (1 or 2), each M rows with its own A and output
-  int tile_n;               // columns of a tile (accumulator columns), a multiple of 64 up to 256
+  int a_mn, b_mn;
+  int first;                // its first tile in the launch
+};
+constexpr int kDenseProblems = 3;
+struct DenseGemmArgs {
+  DenseProblem p[kDenseProblems];   // products of one launch (the epilogue's inputs below are the first one's)
+  int problems, tiles;      // tiles of all
+  int balanced;             // CTAs (pairs) take consecutive tiles of equal work instead of every n-th tile
+  int tile_n;               // columns of a tile (accumulator columns), a multiple of 32 up to 256
   int f16;                  // 16-bit type: 0 bf16, 1 f16
   int fn;                   // moe_fn
   int out_f32;              // out[] in fp32 instead of the 16-bit type
   int saved8;               // kEpiGlu writes / kEpiDGlu reads g and u as 8-bit checkpoints
   const void* bias;         // [N] 16-bit or NULL
   const void* residual;     // [M, ldr] 16-bit or NULL
-  void* out[2];             // kEpiLinear: per row segment; kEpiGlu: h; kEpiDGlu: dg, du
+  int64_t ldr;              // row pitch in elements
   void* pre;                // kEpiLinear: D + bias [M, N] 16-bit or NULL; kEpiDGlu: h
   void* g;                  // kEpiGlu out (or NULL) / kEpiDGlu in: [M, N] 16-bit, or E4M3 codes
   void* u;
   uint8_t* g_s;             // E8M0 scales [M, ceil(N/32)] of the codes
   uint8_t* u_s;
-  int64_t ldr, ldo;         // row pitches in elements
   int32_t* status;
 };
 
-template <int kEpi, bool kAMn, bool kBMn, int kCg>
+template <int kEpi, int kCg>
 __global__ void k_dense_gemm(const __grid_constant__ DenseGemmArgs a);
 size_t dense_gemm_smem_bytes();
 int dense_gemm_threads();
 
 // --- few tokens (dense_rows.cu) -------------------------------------------------
-// The weights are the MMA's 128 rows (map_a; kEpiGlu: 64 gate and 64 up rows),
-// the tokens its columns (map_b[0], tile_n = T rounded up to 16). A cluster of
+// Problem 0 with the sides exchanged: the weights are the MMA's 128 rows (map_a;
+// kEpiGlu: 64 gate and 64 up rows), the tokens its columns (map_b[0], tile_n = T rounded up to 16). A cluster of
 // `splits` CTAs divides K and adds its partial sums through shared memory.
 // M, N, K as above (M tokens, N outputs); early: the weights are not written
 // by the previous kernel of the stream and may be loaded before it ends.
 struct DenseRowsArgs {
   DenseGemmArgs g;
   int splits, stages, early;
-  const void* next;         // what the next kernel of the call streams, for L2 (16-byte aligned, or NULL)
-  uint64_t next_bytes;      // a multiple of 16
 };
 constexpr int kRowsSplits = 8;          // most CTAs of a cluster
 constexpr int kRowsTokens = 64;         // most tokens of this kernel
@@ -107,6 +116,6 @@ struct Ckpt8Args {
 };
 __global__ void k_ckpt8_pack(Ckpt8Args a);
 __global__ void k_ckpt8_unpack(Ckpt8Args a);
-constexpr int kCkptThreads = 256;
+constexpr int kCkptThreads = 256, kCkptSpan = 4 * kCkptThreads;   // groups of 8 elements a block takes at a time
 
 }  // namespace moe

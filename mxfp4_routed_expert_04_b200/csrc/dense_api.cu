@@ -45,7 +45,6 @@ char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
   } while (0)
 
 constexpr size_t kStatusBytes = 256;
-constexpr uint64_t kPrefetchMax = 64u << 20;   // about half of the L2
 
 moe_status check_width(const char* name, int v) {
   if (v < 8 || v > 65536 || v % 8 != 0)
@@ -154,13 +153,13 @@ struct Device {
 std::mutex g_mu;
 Device g_dev[64];
 
-template <int kEpi, bool kAMn, bool kBMn>
+template <int kEpi>
 cudaError_t allow_smem() {
   const int bytes = (int)moe::dense_gemm_smem_bytes();
-  const cudaError_t e = cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, kAMn, kBMn, 1>,
+  const cudaError_t e = cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, 1>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, kAMn, kBMn, 2>,
+                          : cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, 2>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
@@ -172,11 +171,9 @@ moe_status device(const Device** out) {
   Device& s = g_dev[dev];
   if (!s.ready) {
     cudaError_t e = cudaDeviceGetAttribute(&s.num_sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, false>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, false, true>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear, true, true>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu, false, false>();
-    if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu, false, true>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu>();
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(moe::k_dense_rows<moe::kEpiLinear>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)moe::dense_rows_smem_bytes());
@@ -251,7 +248,32 @@ struct Mat {
   int64_t rows, cols, ld;
 };
 
-// Tile of a product: a pair's 256 rows or one CTA's 128, and the columns, from
+// A launch of products: collected first, then given a tile and enqueued.
+struct Launch {
+  moe::DenseGemmArgs g;
+  Mat a[moe::kDenseProblems][2], b[moe::kDenseProblems][2];
+  int na[moe::kDenseProblems], nb[moe::kDenseProblems];
+
+  Launch(int f16, void* ws) {
+    memset(&g, 0, sizeof(g));
+    g.f16 = f16;
+    g.status = static_cast<int32_t*>(ws);
+  }
+  moe::DenseProblem& add(int M, int N, int K, bool a_mn, const Mat* am, int an, bool b_mn, const Mat* bm, int bn) {
+    const int i = g.problems++;
+    moe::DenseProblem& p = g.p[i];
+    p.M = M; p.N = N; p.K = K;
+    p.k_segs = 1; p.m_segs = 1;
+    p.a_mn = a_mn; p.b_mn = b_mn;
+    na[i] = an;
+    nb[i] = bn;
+    for (int k = 0; k < an; ++k) a[i][k] = am[k];
+    for (int k = 0; k < bn; ++k) b[i][k] = bm[k];
+    return p;
+  }
+};
+
+// Tile of a launch: a pair's 256 rows or one CTA's 128, and the columns, from
 // the time of a wave of tiles in a long product. That time grows with the
 // columns (MMAs) and with a constant (the A rows every tile loads): measured at
 // 4096 x 4096 x 8192, pairs of 256 / 192 / 160 / 128 columns 188 / 189 / 197 /
@@ -260,17 +282,36 @@ struct Mat {
 struct TileChoice {
   int cg, n;
 };
-TileChoice pick_tile(const Device& dv, int M, int m_segs, long N, bool glu, bool b_mn) {
+long tiles_of(const moe::DenseProblem& p, int cg, int cols) {
+  return p.m_segs * (long)((p.M + 128 * cg - 1) / (128 * cg)) * ((p.N + cols - 1) / cols);
+}
+long stages_of(const moe::DenseProblem& p) { return (p.K + 63) / 64 * (long)p.k_segs; }
+TileChoice pick_tile(const Device& dv, const moe::DenseGemmArgs& g, bool glu) {
   TileChoice best = {1, 64};
   long best_cost = -1;
-  for (int cg = M > 128 ? 2 : 1; cg >= 1; --cg) {
+  int rows = 0, longest = 0;
+  bool b_mn = false;
+  for (int i = 0; i < g.problems; ++i) {
+    rows = std::max(rows, g.p[i].M);
+    longest = std::max<int>(longest, (int)stages_of(g.p[i]));
+    b_mn |= g.p[i].b_mn != 0;
+  }
+  for (int cg = rows > 128 ? 2 : 1; cg >= 1; --cg) {
     for (int n = 256; n >= 64; n -= 32) {
       if (b_mn && n % (64 * cg) != 0) continue;
       if (glu && n % 64 != 0) continue;
-      const long cols = glu ? n / 2 : n;
-      const long tiles = m_segs * (long)((M + 128 * cg - 1) / (128 * cg)) * ((N + cols - 1) / cols);
-      const long slots = dv.num_sms / cg, waves = (tiles + slots - 1) / slots;
-      const long cost = waves * (cg == 2 ? 100L * (n + 100) : 107L * (n + 136));
+      const long slots = dv.num_sms / cg;
+      long work = 0, tiles = 0;
+      for (int i = 0; i < g.problems; ++i) {
+        const long t = tiles_of(g.p[i], cg, glu ? n / 2 : n);
+        tiles += t;
+        work += t * stages_of(g.p[i]);
+      }
+      // stages of the fullest slot: whole waves of one product; of several, an
+      // even share and the tile that ends it
+      const long stages = g.problems == 1 ? (tiles + slots - 1) / slots * longest
+                                          : std::max<long>(longest, (work + slots - 1) / slots + longest / 2);
+      const long cost = stages * (cg == 2 ? 100L * (n + 100) : 107L * (n + 136));
       if (best_cost < 0 || cost < best_cost) {
         best_cost = cost;
         best = {cg, n};
@@ -280,90 +321,114 @@ TileChoice pick_tile(const Device& dv, int M, int m_segs, long N, bool glu, bool
   return best;
 }
 
-template <int kEpi, bool kAMn, bool kBMn>
-moe_status gemm(const Device& dv, moe::DenseGemmArgs& g, const Mat* a, int na, const Mat* b, int nb,
-                cudaStream_t st, const char* what) {
-  constexpr bool glu = kEpi == moe::kEpiGlu;
-  const TileChoice t = pick_tile(dv, g.M, g.m_segs, g.N, glu, kBMn);
+// Tensor maps and tile numbers of a launch's products for tile `t`; returns the tiles.
+moe_status place(Launch& l, const TileChoice& t, bool glu, long* tiles, const char* what) {
+  moe::DenseGemmArgs& g = l.g;
   g.tile_n = t.n;
-  for (int i = 0; i < na; ++i)
-    TRY(map16(&g.map_a[i], a[i].p, g.f16, a[i].rows, a[i].cols, a[i].ld, kAMn ? 64 : 128, what));
-  for (int i = 0; i < nb; ++i)
-    TRY(map16(&g.map_b[i], b[i].p, g.f16, b[i].rows, b[i].cols, b[i].ld,
-              kBMn ? 64 : glu ? t.n / 2 : t.n / t.cg, what));
-  const int cols = glu ? t.n / 2 : t.n, rows = 128 * t.cg;
-  const long tiles = (long)g.m_segs * ((g.M + rows - 1) / rows) * ((g.N + cols - 1) / cols);
-  const int ctas = (int)std::min<long>(tiles, dv.num_sms / t.cg) * t.cg;
-  return launch(what, t.cg == 2 ? moe::k_dense_gemm<kEpi, kAMn, kBMn, 2> : moe::k_dense_gemm<kEpi, kAMn, kBMn, 1>,
-                dim3((unsigned)ctas), moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), t.cg, st, g);
+  *tiles = 0;
+  for (int i = 0; i < g.problems; ++i) {
+    moe::DenseProblem& p = g.p[i];
+    p.first = (int)*tiles;
+    *tiles += tiles_of(p, t.cg, glu ? t.n / 2 : t.n);
+    for (int k = 0; k < l.na[i]; ++k) {
+      const Mat& m = l.a[i][k];
+      TRY(map16(&p.map_a[k], m.p, g.f16, m.rows, m.cols, m.ld, p.a_mn ? 64 : 128, what));
+    }
+    for (int k = 0; k < l.nb[i]; ++k) {
+      const Mat& m = l.b[i][k];
+      TRY(map16(&p.map_b[k], m.p, g.f16, m.rows, m.cols, m.ld, p.b_mn ? 64 : glu ? t.n / 2 : t.n / t.cg, what));
+    }
+  }
+  g.tiles = (int)*tiles;
+  return MOE_OK;
+}
+
+template <int kEpi>
+moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* what) {
+  constexpr bool glu = kEpi == moe::kEpiGlu;
+  moe::DenseGemmArgs& g = l.g;
+  const TileChoice t = pick_tile(dv, g, glu);
+  const long slots = dv.num_sms / t.cg;
+  long tiles = 0;
+  for (int i = 0; i < g.problems; ++i) tiles += tiles_of(g.p[i], t.cg, t.n);
+  // Several products go in one launch, in equal shares of their stages, while
+  // they are a few waves together; longer ones keep their own launches, whose
+  // neighbouring tiles share operands in L2 (gradients at T = 777, 1000 x 1352:
+  // 63 us in three launches, 49 in one; at 4096, 8192 x 2048: 682 and 691).
+  if (g.problems > 1 && tiles >= 4 * slots) {
+    for (int i = 0; i < g.problems; ++i) {
+      Launch one = l;
+      one.g.problems = 1;
+      one.g.p[0] = g.p[i];
+      one.na[0] = l.na[i];
+      one.nb[0] = l.nb[i];
+      for (int k = 0; k < 2; ++k) {
+        one.a[0][k] = l.a[i][k];
+        one.b[0][k] = l.b[i][k];
+      }
+      TRY(enqueue<kEpi>(dv, one, st, what));
+    }
+    return MOE_OK;
+  }
+  TRY(place(l, t, glu, &tiles, what));
+  g.balanced = g.problems > 1;
+  const int ctas = (int)std::min<long>(tiles, slots) * t.cg;
+  return launch(what, t.cg == 2 ? moe::k_dense_gemm<kEpi, 2> : moe::k_dense_gemm<kEpi, 1>, dim3((unsigned)ctas),
+                moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), t.cg, st, g);
 }
 
 // Few tokens: the weights' rows over clusters that split K, so that up to two
 // CTAs of every SM stream (each at least four stages of 64 k).
 template <int kEpi>
-moe_status rows(const Device& dv, const moe::DenseGemmArgs& g, const Mat& x, const Mat* w, bool early,
-                const Mat* next, cudaStream_t st, const char* what) {
+moe_status rows(const Device& dv, const Launch& l, bool early, cudaStream_t st, const char* what) {
   constexpr bool glu = kEpi == moe::kEpiGlu;
   moe::DenseRowsArgs r;
-  r.g = g;
-  r.g.tile_n = (g.M + 15) / 16 * 16;
+  r.g = l.g;
   r.early = early;
-  r.next = next ? next->p : nullptr;
-  r.next_bytes = next ? std::min<uint64_t>((uint64_t)next->rows * next->cols * 2, kPrefetchMax) : 0;
-  TRY(map16(&r.g.map_b[0], x.p, g.f16, x.rows, x.cols, x.ld, r.g.tile_n, what));
+  moe::DenseProblem& p = r.g.p[0];
+  r.g.tile_n = (p.M + 15) / 16 * 16;
+  const Mat &x = l.a[0][0], *w = l.b[0];
+  TRY(map16(&p.map_b[0], x.p, r.g.f16, x.rows, x.cols, x.ld, r.g.tile_n, what));
   for (int i = 0; i < (glu ? 2 : 1); ++i)
-    TRY(map16(&r.g.map_a[i], w[i].p, g.f16, w[i].rows, w[i].cols, w[i].ld, glu ? 64 : 128, what));
-  const int tile = glu ? 64 : 128, tiles = (g.N + tile - 1) / tile, ks = (g.K + 63) / 64;
+    TRY(map16(&p.map_a[i], w[i].p, r.g.f16, w[i].rows, w[i].cols, w[i].ld, glu ? 64 : 128, what));
+  const int tile = glu ? 64 : 128, tiles = (p.N + tile - 1) / tile, ks = (p.K + 63) / 64;
   r.splits = std::max(1, std::min(std::min(moe::kRowsSplits, 7 * dv.num_sms / 4 / tiles), ks / 4));
-  r.stages = moe::dense_rows_stages(g.M, r.g.tile_n);
+  r.stages = moe::dense_rows_stages(p.M, r.g.tile_n);
   return launch(what, moe::k_dense_rows<kEpi>, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads,
                 moe::dense_rows_smem_bytes(), r.splits, st, r);
-}
-
-moe::DenseGemmArgs gemm_args(int M, int N, int K, int f16, void* ws) {
-  moe::DenseGemmArgs g;
-  memset(&g, 0, sizeof(g));
-  g.M = M; g.N = N; g.K = K; g.f16 = f16;
-  g.k_segs = 1; g.m_segs = 1;
-  g.status = static_cast<int32_t*>(ws);
-  return g;
 }
 
 // y[T, N] = f(x W^T + bias) + residual
 moe_status project(const Device& dv, int T, int N, int K, int f16, int fn, int out_f32, const void* x, int64_t ldx,
                    const void* w, const void* bias, const void* residual, int64_t ldr, void* y, int64_t ldy,
                    void* pre, void* ws, cudaStream_t st, const char* what, bool early = false) {
-  moe::DenseGemmArgs g = gemm_args(T, N, K, f16, ws);
-  g.fn = fn; g.out_f32 = out_f32; g.bias = bias; g.residual = residual; g.ldr = ldr;
-  g.out[0] = y; g.ldo = ldy; g.pre = pre;
+  Launch l(f16, ws);
   const Mat a = {x, T, K, ldx}, b = {w, N, K, K};
-  if (T <= moe::kRowsTokens) return rows<moe::kEpiLinear>(dv, g, a, &b, early, nullptr, st, what);
-  return gemm<moe::kEpiLinear, false, false>(dv, g, &a, 1, &b, 1, st, what);
+  moe::DenseProblem& p = l.add(T, N, K, false, &a, 1, false, &b, 1);
+  p.out[0] = y; p.ldo = ldy;
+  l.g.fn = fn; l.g.out_f32 = out_f32; l.g.bias = bias; l.g.residual = residual; l.g.ldr = ldr; l.g.pre = pre;
+  return T <= moe::kRowsTokens ? rows<moe::kEpiLinear>(dv, l, early, st, what)
+                               : enqueue<moe::kEpiLinear>(dv, l, st, what);
 }
 
 // dx[T, K] = sum_s dz_s[T, N] W_s[N, K]
-moe_status input_grad(const Device& dv, int T, int N, int K, int f16, int out_f32, const Mat* dz, const Mat* w,
-                      int segs, void* dx, int64_t lddx, void* ws, cudaStream_t st, const char* what) {
-  moe::DenseGemmArgs g = gemm_args(T, K, N, f16, ws);
-  g.k_segs = segs; g.out_f32 = out_f32; g.out[0] = dx; g.ldo = lddx;
-  return gemm<moe::kEpiLinear, false, true>(dv, g, dz, segs, w, segs, st, what);
+void add_input_grad(Launch& l, int T, int N, int K, const Mat* dz, const Mat* w, int segs, void* dx, int64_t lddx) {
+  moe::DenseProblem& p = l.add(T, K, N, false, dz, segs, true, w, segs);
+  p.k_segs = segs; p.out[0] = dx; p.ldo = lddx;
 }
 
 // dw_s[N, K] = dz_s[T, N]^T x[T, K]
-moe_status weight_grad(const Device& dv, int T, int N, int K, int f16, int out_f32, const Mat* dz, int segs,
-                       const Mat& x, void* dw0, void* dw1, void* ws, cudaStream_t st, const char* what) {
-  moe::DenseGemmArgs g = gemm_args(N, K, T, f16, ws);
-  g.m_segs = segs; g.out_f32 = out_f32; g.out[0] = dw0; g.out[1] = dw1; g.ldo = K;
-  return gemm<moe::kEpiLinear, true, true>(dv, g, dz, segs, &x, 1, st, what);
+void add_weight_grad(Launch& l, int T, int N, int K, const Mat* dz, int segs, const Mat& x, void* dw0, void* dw1) {
+  moe::DenseProblem& p = l.add(N, K, T, true, dz, segs, true, &x, 1);
+  p.m_segs = segs; p.out[0] = dw0; p.out[1] = dw1; p.ldo = K;
 }
 
 moe_status ckpt8(const Device& dv, bool pack, int f16, int64_t rows, int cols, const void* src, void* dst, int64_t ld,
                  uint8_t* q, uint8_t* s, cudaStream_t st) {
   moe::Ckpt8Args c;
   c.src = src; c.dst = dst; c.q = q; c.s = s; c.rows = rows; c.ld = ld; c.cols = cols; c.f16 = f16;
-  const int64_t items = rows * (pack ? (cols + 31) / 32 : cols / 8);
-  const int64_t blocks = std::min<int64_t>((items + moe::kCkptThreads - 1) / moe::kCkptThreads,
-                                           (int64_t)dv.num_sms * 16);
+  const int64_t spans = (rows * ((cols + 31) / 32 * 4) + moe::kCkptSpan - 1) / moe::kCkptSpan;
+  const int64_t blocks = std::min<int64_t>(spans, 1 << 20);
   return launch(pack ? "checkpoint pack" : "checkpoint unpack", pack ? moe::k_ckpt8_pack : moe::k_ckpt8_unpack,
                 dim3((unsigned)blocks), moe::kCkptThreads, 0, 1, st, c);
 }
@@ -476,19 +541,17 @@ moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dy, cons
                dim3((unsigned)((p.N + moe::kDzCols - 1) / moe::kDzCols), (unsigned)p.dz_chunks), moe::kDzThreads, 0, 1,
                st, z));
     if (dbias)
-      TRY(launch("bias gradient", moe::k_colsum, dim3((unsigned)((p.N + 255) / 256)), 256, 0, 1, st,
+      TRY(launch("bias gradient", moe::k_colsum, dim3((unsigned)((p.N + 31) / 32)), 256, 0, 1, st,
                  (const float*)z.part, p.dz_chunks, p.N, p.f16, p.out_f32, dbias));
     if (z.dz) dz = {z.dz, p.T, p.N, p.N};
   }
-  if (dx) {
-    const Mat wm = {w, p.N, p.K, p.K};
-    TRY(input_grad(*dv, p.T, p.N, p.K, p.f16, p.out_f32, &dz, &wm, 1, dx, p.ldx, ws, st, "input gradient"));
-  }
-  if (dw) {
-    const Mat xm = {x, p.T, p.K, p.ldx};
-    TRY(weight_grad(*dv, p.T, p.N, p.K, p.f16, p.out_f32, &dz, 1, xm, dw, nullptr, ws, st, "weight gradient"));
-  }
-  return MOE_OK;
+  if (!dx && !dw) return MOE_OK;
+  Launch l(p.f16, ws);
+  l.g.out_f32 = p.out_f32;
+  const Mat wm = {w, p.N, p.K, p.K}, xm = {x, p.T, p.K, p.ldx};
+  if (dx) add_input_grad(l, p.T, p.N, p.K, &dz, &wm, 1, dx, p.ldx);
+  if (dw) add_weight_grad(l, p.T, p.N, p.K, &dz, 1, xm, dw, nullptr);
+  return enqueue<moe::kEpiLinear>(*dv, l, st, "projection gradients");
 }
 
 moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, const void* wu, const void* wd,
@@ -510,18 +573,18 @@ moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, cons
   TRY(device(&dv));
   cudaStream_t st = (cudaStream_t)stream;
   void* h = at(ws, p.off_h);
-  moe::DenseGemmArgs g = gemm_args(p.T, p.I, p.H, p.f16, ws);
-  g.fn = p.fn; g.out[0] = h;
-  if (saved) {
-    g.g = saved->g; g.u = saved->u; g.g_s = saved->g_s; g.u_s = saved->u_s;
-    g.saved8 = p.save == MOE_SAVE_8;
-  }
+  Launch l(p.f16, ws);
   const Mat xm = {x, p.T, p.H, p.ldx};
   const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}};
-  const Mat wdm = {wd, p.H, p.I, p.I};
-  const bool few = p.T <= moe::kRowsTokens;
-  TRY(few ? rows<moe::kEpiGlu>(*dv, g, xm, wm, false, &wdm, st, "gate/up projection")
-          : (gemm<moe::kEpiGlu, false, false>(*dv, g, &xm, 1, wm, 2, st, "gate/up projection")));
+  moe::DenseProblem& gu = l.add(p.T, p.I, p.H, false, &xm, 1, false, wm, 2);
+  gu.out[0] = h; gu.ldo = p.I;
+  l.g.fn = p.fn;
+  if (saved) {
+    l.g.g = saved->g; l.g.u = saved->u; l.g.g_s = saved->g_s; l.g.u_s = saved->u_s;
+    l.g.saved8 = p.save == MOE_SAVE_8;
+  }
+  TRY(p.T <= moe::kRowsTokens ? rows<moe::kEpiGlu>(*dv, l, false, st, "gate/up projection")
+                              : enqueue<moe::kEpiGlu>(*dv, l, st, "gate/up projection"));
   if (saved && saved->x_q)
     TRY(ckpt8(*dv, true, p.f16, p.T, p.H, x, nullptr, p.ldx, saved->x_q, saved->x_s, st));
   return project(*dv, p.T, p.H, p.I, p.f16, MOE_FN_NONE, p.out_f32, h, p.I, wd, nullptr, residual, p.ldr, y, p.ldy,
@@ -560,24 +623,23 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dy, const void
     TRY(ckpt8(*dv, false, p.f16, p.T, p.H, nullptr, at(ws, p.off_x), p.H, saved->x_q, saved->x_s, st));
     xm = {at(ws, p.off_x), p.T, p.H, p.H};
   }
-  moe::DenseGemmArgs g = gemm_args(p.T, p.I, p.H, p.f16, ws);
-  g.fn = p.fn; g.saved8 = p.save == MOE_SAVE_8;
-  g.g = saved->g; g.u = saved->u; g.g_s = saved->g_s; g.u_s = saved->u_s;
-  g.out[0] = at(ws, p.off_dg); g.out[1] = at(ws, p.off_du); g.pre = at(ws, p.off_h);
+  void *dg = at(ws, p.off_dg), *du = at(ws, p.off_du), *h = at(ws, p.off_h);
+  Launch hidden(p.f16, ws);
   const Mat wdm = {wd, p.H, p.I, p.I};
-  TRY((gemm<moe::kEpiDGlu, false, true>(*dv, g, &dym, 1, &wdm, 1, st, "hidden gradient")));
-  const Mat dgu[2] = {{g.out[0], p.T, p.I, p.I}, {g.out[1], p.T, p.I, p.I}};
-  if (dx) {
-    const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}};
-    TRY(input_grad(*dv, p.T, p.I, p.H, p.f16, p.out_f32, dgu, wm, 2, dx, p.ldx, ws, st, "input gradient"));
-  }
-  if (dwg)
-    TRY(weight_grad(*dv, p.T, p.I, p.H, p.f16, p.out_f32, dgu, 2, xm, dwg, dwu, ws, st, "gate/up weight gradient"));
-  if (dwd) {
-    const Mat hm = {g.pre, p.T, p.I, p.I};
-    TRY(weight_grad(*dv, p.T, p.H, p.I, p.f16, p.out_f32, &dym, 1, hm, dwd, nullptr, ws, st, "down weight gradient"));
-  }
-  return MOE_OK;
+  moe::DenseProblem& dh = hidden.add(p.T, p.I, p.H, false, &dym, 1, true, &wdm, 1);
+  dh.out[0] = dg; dh.out[1] = du; dh.ldo = p.I;
+  hidden.g.fn = p.fn; hidden.g.saved8 = p.save == MOE_SAVE_8; hidden.g.pre = h;
+  hidden.g.g = saved->g; hidden.g.u = saved->u; hidden.g.g_s = saved->g_s; hidden.g.u_s = saved->u_s;
+  TRY(enqueue<moe::kEpiDGlu>(*dv, hidden, st, "hidden gradient"));
+  // the three products that read it, in one launch
+  Launch l(p.f16, ws);
+  l.g.out_f32 = p.out_f32;
+  const Mat dgu[2] = {{dg, p.T, p.I, p.I}, {du, p.T, p.I, p.I}};
+  const Mat wm[2] = {{wg, p.I, p.H, p.H}, {wu, p.I, p.H, p.H}}, hm = {h, p.T, p.I, p.I};
+  if (dx) add_input_grad(l, p.T, p.I, p.H, dgu, wm, 2, dx, p.ldx);
+  if (dwg) add_weight_grad(l, p.T, p.I, p.H, dgu, 2, xm, dwg, dwu);
+  if (dwd) add_weight_grad(l, p.T, p.H, p.I, &dym, 1, hm, dwd, nullptr);
+  return enqueue<moe::kEpiLinear>(*dv, l, st, "block gradients");
 }
 
 moe_status moe_ckpt8_pack(int32_t dtype, int64_t rows, int32_t cols, const void* src, int64_t ld,

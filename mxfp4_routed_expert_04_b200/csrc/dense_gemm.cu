@@ -20,6 +20,8 @@
 // epilogue out of one accumulator buffer while the next tile fills the other.
 // Every wait is bounded; a wait that gives up raises the CTA's abort flag and
 // the status word.
+#include <type_traits>
+
 #include "dense.cuh"
 
 namespace moe {
@@ -34,8 +36,21 @@ constexpr int kRing = 192 * 1024;
 constexpr int kGroupM = 8;                         // row tiles that share their column tiles in L2
 
 struct Tile {
-  int seg, m0, n0;
+  int prob, seg, m0, n0;
 };
+// f(a_mn, b_mn) as compile-time constants: the directions that the launches use
+template <int kEpi, typename F>
+MOE_DEV void by_direction(const DenseProblem& p, F&& f) {
+  using K = std::false_type;
+  using MN = std::true_type;
+  if constexpr (kEpi == kEpiGlu) f(K(), K());
+  else if constexpr (kEpi == kEpiDGlu) f(K(), MN());
+  else if (p.a_mn) f(MN(), MN());
+  else if (p.b_mn) f(K(), MN());
+  else f(K(), K());
+}
+// 64-k stages of a tile, its contraction segments one after the other
+MOE_DEV int stages_of(const DenseProblem& p) { return (p.K + 63) / 64 * p.k_segs; }
 
 }  // namespace
 
@@ -49,6 +64,7 @@ struct Tile {
 // bias and a residual took 147 us, without them 106).
 struct EpiPos {
   int row, col;             // first row and column of the 32 x 32 block
+  int M, N;                 // the problem's extents
 };
 struct EpiIn {
   uint4 a[4], b[4];         // kEpiLinear: residual, bias; kEpiDGlu: g, u
@@ -74,7 +90,7 @@ MOE_DEV void sts8b(uint32_t addr, uint2 v) {
 MOE_DEV bool piece(const DenseGemmArgs& a, const EpiPos& e, int i, int lane, int& r, int& c) {
   r = e.row + 8 * i + (lane >> 2);
   c = e.col + 8 * (lane & 3);
-  return r < a.M && c < a.N;
+  return r < e.M && c < e.N;
 }
 MOE_DEV void fetch16(const DenseGemmArgs& a, const EpiPos& e, const void* base, int64_t ld, int lane, uint4 (&v)[4]) {
 #pragma unroll
@@ -91,7 +107,7 @@ MOE_DEV void fetch8(const DenseGemmArgs& a, const EpiPos& e, const void* base, i
     int r, c;
     v[i] = make_uint4(0u, 0u, 0u, 0u);
     if (piece(a, e, i, lane, r, c)) {
-      const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + (size_t)r * a.N + c));
+      const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + (size_t)r * e.N + c));
       v[i].x = w.x;
       v[i].y = w.y;
     }
@@ -138,7 +154,7 @@ MOE_DEV void put32(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int la
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = 4 * i + (lane >> 3), c = e.col + 4 * (lane & 7);
-    if (e.row + r < a.M && c < a.N)
+    if (e.row + r < e.M && c < e.N)
       *reinterpret_cast<uint4*>(static_cast<float*>(base) + (size_t)(e.row + r) * ld + c) =
           lds16(stage128(buf, r, lane & 7));
   }
@@ -151,7 +167,7 @@ MOE_DEV void put8(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lan
   for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   const uint32_t code = e4m3_scale_code(m);
   const float inv = e4m3_inv_scale(code);
-  if (e.row + lane < a.M && e.col < a.N) s[(size_t)(e.row + lane) * ((a.N + 31) / 32) + e.col / 32] = (uint8_t)code;
+  if (e.row + lane < e.M && e.col < e.N) s[(size_t)(e.row + lane) * ((e.N + 31) / 32) + e.col / 32] = (uint8_t)code;
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -161,7 +177,7 @@ MOE_DEV void put8(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lan
   for (int i = 0; i < 4; ++i) {
     int r, c;
     if (piece(a, e, i, lane, r, c))
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q) + (size_t)r * a.N + c) =
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(q) + (size_t)r * e.N + c) =
           lds8b(stage32(buf, 8 * i + (lane >> 2), lane & 3));
   }
 }
@@ -178,7 +194,7 @@ MOE_DEV void epi_fetch(const DenseGemmArgs& a, const EpiPos& e, int lane, EpiIn&
     if (a.bias) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        in.b[j] = e.col + 8 * j < a.N ? ldg16(static_cast<const uint16_t*>(a.bias) + e.col + 8 * j)
+        in.b[j] = e.col + 8 * j < e.N ? ldg16(static_cast<const uint16_t*>(a.bias) + e.col + 8 * j)
                                       : make_uint4(0u, 0u, 0u, 0u);
     }
   }
@@ -187,19 +203,19 @@ MOE_DEV void epi_fetch(const DenseGemmArgs& a, const EpiPos& e, int lane, EpiIn&
       fetch8(a, e, a.g, lane, in.a);
       fetch8(a, e, a.u, lane, in.b);
       in.sa = in.sb = 0.0f;
-      if (e.row + lane < a.M && e.col < a.N) {
-        const size_t so = (size_t)(e.row + lane) * ((a.N + 31) / 32) + e.col / 32;
+      if (e.row + lane < e.M && e.col < e.N) {
+        const size_t so = (size_t)(e.row + lane) * ((e.N + 31) / 32) + e.col / 32;
         in.sa = e8m0_to_f32(__ldg(a.g_s + so));
         in.sb = e8m0_to_f32(__ldg(a.u_s + so));
       }
     } else {
-      fetch16(a, e, a.g, a.N, lane, in.a);
-      fetch16(a, e, a.u, a.N, lane, in.b);
+      fetch16(a, e, a.g, e.N, lane, in.a);
+      fetch16(a, e, a.u, e.N, lane, in.b);
     }
   }
 }
 
-MOE_DEV void epi_linear(const DenseGemmArgs& a, int seg, const EpiPos& e, uint32_t buf, int lane, const EpiIn& in,
+MOE_DEV void epi_linear(const DenseGemmArgs& a, const DenseProblem& p, int seg, const EpiPos& e, uint32_t buf, int lane, const EpiIn& in,
                         float (&v)[32]) {
   if (a.bias) {
 #pragma unroll
@@ -210,11 +226,8 @@ MOE_DEV void epi_linear(const DenseGemmArgs& a, int seg, const EpiPos& e, uint32
       for (int i = 0; i < 8; ++i) v[8 * j + i] += t[i];
     }
   }
-  if (a.pre) put16(a, e, buf, lane, v, a.pre, a.N);
-  if (a.fn) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = fn_value(a.fn, v[i]);
-  }
+  if (a.pre) put16(a, e, buf, lane, v, a.pre, e.N);
+  fn_values(a.fn, v);
   if (a.residual) {
     __syncwarp();
     pieces_to_stage(buf, lane, in.a);
@@ -227,8 +240,8 @@ MOE_DEV void epi_linear(const DenseGemmArgs& a, int seg, const EpiPos& e, uint32
       for (int i = 0; i < 8; ++i) v[8 * j + i] += t[i];
     }
   }
-  if (a.out_f32) put32(a, e, buf, lane, v, a.out[seg], a.ldo);
-  else put16(a, e, buf, lane, v, a.out[seg], a.ldo);
+  if (a.out_f32) put32(a, e, buf, lane, v, p.out[seg], p.ldo);
+  else put16(a, e, buf, lane, v, p.out[seg], p.ldo);
 }
 
 MOE_DEV void epi_glu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, float (&g)[32], float (&u)[32]) {
@@ -237,13 +250,14 @@ MOE_DEV void epi_glu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int 
       put8(a, e, buf, lane, g, a.g, a.g_s);
       put8(a, e, buf + 2048, lane, u, a.u, a.u_s);
     } else {
-      put16(a, e, buf, lane, g, a.g, a.N);
-      put16(a, e, buf + 2048, lane, u, a.u, a.N);
+      put16(a, e, buf, lane, g, a.g, e.N);
+      put16(a, e, buf + 2048, lane, u, a.u, e.N);
     }
   }
+  fn_values(a.fn, g);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) g[i] = fn_value(a.fn, g[i]) * u[i];
-  put16(a, e, buf, lane, g, a.out[0], a.N);
+  for (int i = 0; i < 32; ++i) g[i] *= u[i];
+  put16(a, e, buf, lane, g, a.p[0].out[0], e.N);
 }
 
 MOE_DEV void epi_dglu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int lane, const EpiIn& in,
@@ -261,7 +275,7 @@ MOE_DEV void epi_dglu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int
   uint4 gq[4], uq[4], hq[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float g[8], u[8], x[8], y[8], h[8];
+    float g[8], u[8], f[8], s[8], x[8], y[8], h[8];
     if (a.saved8) {
       const uint2 p = lds8b(stage32(ga, lane, j)), q = lds8b(stage32(ua, lane, j));
       e4m3_unquad(p.x, in.sa, g);
@@ -272,13 +286,12 @@ MOE_DEV void epi_dglu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int
       unpack16x8(a.f16, lds16(stage64(ga, lane, j)), g);
       unpack16x8(a.f16, lds16(stage64(ua, lane, j)), u);
     }
+    fn_slopes(a.fn, g, f, s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float f, s;
-      fn_slope(a.fn, g[i], f, s);
-      x[i] = dh[8 * j + i] * u[i] * s;
-      y[i] = dh[8 * j + i] * f;
-      h[i] = f * u[i];
+      x[i] = dh[8 * j + i] * u[i] * s[i];
+      y[i] = dh[8 * j + i] * f[i];
+      h[i] = f[i] * u[i];
     }
     gq[j] = pack16x8(a.f16, x);
     uq[j] = pack16x8(a.f16, y);
@@ -291,16 +304,16 @@ MOE_DEV void epi_dglu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int
     sts16(stage64(ua, lane, j), uq[j]);
   }
   __syncwarp();
-  flush16(a, e, ga, lane, a.out[0], a.N);
-  flush16(a, e, ua, lane, a.out[1], a.N);
+  flush16(a, e, ga, lane, a.p[0].out[0], e.N);
+  flush16(a, e, ua, lane, a.p[0].out[1], e.N);
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 4; ++j) sts16(stage64(ga, lane, j), hq[j]);
   __syncwarp();
-  flush16(a, e, ga, lane, a.pre, a.N);
+  flush16(a, e, ga, lane, a.pre, e.N);
 }
 
-template <int kEpi, bool kAMn, bool kBMn, int kCg>
+template <int kEpi, int kCg>
 __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constant__ DenseGemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -329,8 +342,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
     mbar_init(&drain, 1);
     abort_flag = 0;
     fence_mbar_init();
-    tc::prefetch_map(&a.map_a[0]);
-    tc::prefetch_map(&a.map_b[0]);
+    for (int i = 0; i < a.problems; ++i) {
+      tc::prefetch_map(&a.p[i].map_a[0]);
+      tc::prefetch_map(&a.p[i].map_b[0]);
+    }
   }
   if (warp == 1) tc::alloc_cg<kCg>(&tmem_slot, 512);
   tc::fence_before_sync();
@@ -341,18 +356,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
   pdl_wait();
   pdl_trigger();
 
-  const int mt1 = (a.M + 128 * kCg - 1) / (128 * kCg);      // row tiles of a segment
-  const int mt = mt1 * a.m_segs, nt = (a.N + cols - 1) / cols;
-  const int tiles = mt * nt;
-  const int ks1 = (a.K + 63) / 64, ks = ks1 * a.k_segs;
-  const int first = (int)blockIdx.x / kCg, step = (int)gridDim.x / kCg;
+  // this CTA's (pair's) tiles
+  const int slot = (int)blockIdx.x / kCg, slots = (int)gridDim.x / kCg;
+  int q0 = slot, q1 = a.tiles, dq = slots;
+  if (a.balanced) {
+    long total = 0;
+    for (int i = 0; i < a.problems; ++i) {
+      const int end = i + 1 < a.problems ? a.p[i + 1].first : a.tiles;
+      total += (long)(end - a.p[i].first) * stages_of(a.p[i]);
+    }
+    auto start = [&](int s) {           // the first tile whose stages begin at or after share s
+      long w = (total * s + slots - 1) / slots;
+      for (int i = 0; i < a.problems; ++i) {
+        const int end = i + 1 < a.problems ? a.p[i + 1].first : a.tiles, ks = stages_of(a.p[i]);
+        const long all = (long)(end - a.p[i].first) * ks;
+        if (w < all) return a.p[i].first + (int)((w + ks - 1) / ks);
+        w -= all;
+      }
+      return a.tiles;
+    };
+    q0 = start(slot);
+    q1 = start(slot + 1);
+    dq = 1;
+  }
   // groups of kGroupM row tiles; in a group the row tiles of one column tile follow each other
   auto tile_of = [&](int q) {
+    Tile t;
+    t.prob = 0;
+    while (t.prob + 1 < a.problems && q >= a.p[t.prob + 1].first) ++t.prob;
+    const DenseProblem& p = a.p[t.prob];
+    q -= p.first;
+    const int mt1 = (p.M + 128 * kCg - 1) / (128 * kCg), mt = mt1 * p.m_segs, nt = (p.N + cols - 1) / cols;
     const int per = kGroupM * nt;
     const int grp = q / per, r = q - grp * per;
     const int gm = min(kGroupM, mt - grp * kGroupM);
     const int n = r / gm, m = grp * kGroupM + r - n * gm;
-    Tile t;
     t.seg = m / mt1;
     t.m0 = (m - t.seg * mt1) * 128 * kCg + 128 * (int)rank;
     t.n0 = n * cols;
@@ -366,42 +404,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
       uint32_t ph = 0;
       long issued = 0;
       bool ok = true;
-      for (int q = first; q < tiles && ok; q += step) {
+      for (int q = q0; q < q1 && ok; q += dq) {
         const Tile t = tile_of(q);
-        for (int j = 0; j < ks; ++j) {
-          if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
-          uint8_t* sa = smem + s * stage_bytes;
-          uint8_t* sb = sa + kATile;
-          const int kseg = j >= ks1 ? 1 : 0;
-          const int k0 = (j - kseg * ks1) * 64;
-          const CUtensorMap* ma = &a.map_a[a.m_segs > 1 ? t.seg : kseg];
-          const CUtensorMap* mb = &a.map_b[kseg];
-          if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(stage_bytes * kCg));
-          auto load = [&](uint8_t* dst, const CUtensorMap* m, int x, int y) {
-            if (kCg == 1) tc::tma_load_2d(dst, m, x, y, &full[s]);
-            else tc::tma_load_2d_pair(dst, m, x, y, tc::mapa(&full[s], 0));
-          };
-          if (kAMn) {
-            load(sa, ma, t.m0, k0);
-            load(sa + 8192, ma, t.m0 + 64, k0);
-          } else {
-            load(sa, ma, k0, t.m0);
-          }
-          if (kEpi == kEpiGlu) {
-            if (kCg == 1) {
-              load(sb, &a.map_b[0], k0, t.n0);
-              load(sb + cols * 128, &a.map_b[1], k0, t.n0);
+        const DenseProblem& p = a.p[t.prob];
+        const int ks1 = (p.K + 63) / 64, ks = ks1 * p.k_segs;
+        auto fill = [&](auto a_mn, auto b_mn) {       // by direction, so the loop has no branches
+          for (int j = 0; j < ks; ++j) {
+            if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
+            uint8_t* sa = smem + s * stage_bytes;
+            uint8_t* sb = sa + kATile;
+            const int kseg = j >= ks1 ? 1 : 0;
+            const int k0 = (j - kseg * ks1) * 64;
+            const CUtensorMap* ma = &p.map_a[p.m_segs > 1 ? t.seg : kseg];
+            const CUtensorMap* mb = &p.map_b[kseg];
+            if (rank == 0) mbar_expect_tx(&full[s], (uint32_t)(stage_bytes * kCg));
+            auto load = [&](uint8_t* dst, const CUtensorMap* m, int x, int y) {
+              if (kCg == 1) tc::tma_load_2d(dst, m, x, y, &full[s]);
+              else tc::tma_load_2d_pair(dst, m, x, y, tc::mapa(&full[s], 0));
+            };
+            if constexpr (a_mn) {
+              load(sa, ma, t.m0, k0);
+              load(sa + 8192, ma, t.m0 + 64, k0);
             } else {
-              load(sb, &a.map_b[rank], k0, t.n0);
+              load(sa, ma, k0, t.m0);
             }
-          } else if (kBMn) {
-            for (int i = 0; i < bn / 64; ++i) load(sb + i * 8192, mb, t.n0 + (int)rank * bn + 64 * i, k0);
-          } else {
-            load(sb, mb, k0, t.n0 + (int)rank * bn);
+            if constexpr (kEpi == kEpiGlu) {
+              if (kCg == 1) {
+                load(sb, &p.map_b[0], k0, t.n0);
+                load(sb + cols * 128, &p.map_b[1], k0, t.n0);
+              } else {
+                load(sb, &p.map_b[rank], k0, t.n0);
+              }
+            } else if constexpr (b_mn) {
+              for (int i = 0; i < bn / 64; ++i) load(sb + i * 8192, mb, t.n0 + (int)rank * bn + 64 * i, k0);
+            } else {
+              load(sb, mb, k0, t.n0 + (int)rank * bn);
+            }
+            ++issued;
+            if (++s == nst) { s = 0; ph ^= 1u; }
           }
-          ++issued;
-          if (++s == nst) { s = 0; ph ^= 1u; }
-        }
+        };
+        by_direction<kEpi>(p, fill);
       }
       // every stage handed back: no arrival of the pair's MMAs is left to come
       for (int i = 0; i < nst && ok; ++i) {
@@ -420,29 +463,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
     // ---------------- MMA issuer ----------------
     // the whole loop in one elected thread
     if (rank == 0 && tc::elect_one()) {
-      const uint32_t idesc = tc::idesc_16(a.f16, 128 * kCg, tn, kAMn, kBMn);
-      constexpr uint32_t a_step = kAMn ? 2048 >> 4 : 32 >> 4, b_step = kBMn ? 2048 >> 4 : 32 >> 4;
       int s = 0, n_it = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int q = first; q < tiles && ok; q += step, ++n_it) {
+      for (int q = q0; q < q1 && ok; q += dq, ++n_it) {
+        const DenseProblem& p = a.p[tile_of(q).prob];
+        const int ks = stages_of(p);
         const int buf = n_it & 1;
         const uint32_t acc_ph = (uint32_t)((n_it >> 1) & 1);
         if (!tc::wait_bounded<(kCg > 1)>(&acc_empty[buf], acc_ph ^ 1u, abort)) break;
         tc::fence_after_sync();
         const uint32_t d = tbase + 256u * buf;
-        for (int j = 0; j < ks; ++j) {
-          if (!tc::wait_bounded(&full[s], ph, abort)) { ok = false; break; }
-          const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kATile;
-          const uint64_t da = kAMn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa);
-          const uint64_t db = kBMn ? tc::desc_mn_sw128(sb, 8192) : tc::desc_sw128(sb);
+        auto issue = [&](auto a_mn, auto b_mn) {
+          const uint32_t idesc = tc::idesc_16(a.f16, 128 * kCg, tn, a_mn, b_mn);
+          constexpr uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+          for (int j = 0; j < ks; ++j) {
+            if (!tc::wait_bounded(&full[s], ph, abort)) { ok = false; break; }
+            const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kATile;
+            const uint64_t da = a_mn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa);
+            const uint64_t db = b_mn ? tc::desc_mn_sw128(sb, 8192) : tc::desc_sw128(sb);
 #pragma unroll
-          for (int kb = 0; kb < 4; ++kb)                    // K = 16 per MMA
-            tc::mma_16<kCg>(d, da + kb * a_step, db + kb * b_step, idesc, (j > 0 || kb > 0) ? 1u : 0u);
-          tc::commit_cg<kCg>(&empty[s]);
-          if (j == ks - 1) tc::commit_cg<kCg>(&acc_full[buf]);
-          if (++s == nst) { s = 0; ph ^= 1u; }
-        }
+            for (int kb = 0; kb < 4; ++kb)                    // K = 16 per MMA
+              tc::mma_16<kCg>(d, da + kb * a_step, db + kb * b_step, idesc, (j > 0 || kb > 0) ? 1u : 0u);
+            tc::commit_cg<kCg>(&empty[s]);
+            if (j == ks - 1) tc::commit_cg<kCg>(&acc_full[buf]);
+            if (++s == nst) { s = 0; ph ^= 1u; }
+          }
+        };
+        by_direction<kEpi>(p, issue);
       }
       if (*abort) {                     // no MMA may run past the CTA's exit
         tc::commit_cg<kCg>(&drain);
@@ -457,10 +505,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
     const uint32_t stage = smem_u32(smem + kRing) + 4096u * (uint32_t)(warp - 2);
     int n_it = 0;
-    for (int q = first; q < tiles; q += step, ++n_it) {
+    for (int q = q0; q < q1; q += dq, ++n_it) {
       const Tile t = tile_of(q);
+      const DenseProblem& p = a.p[t.prob];
       const int buf = n_it & 1;
-      EpiPos e = {t.m0 + 32 * wq, t.n0 + cfirst};
+      EpiPos e = {t.m0 + 32 * wq, t.n0 + cfirst, p.M, p.N};
       EpiIn in;
       if (cfirst < cols) epi_fetch<kEpi>(a, e, lane, in);
       const bool ok = tc::wait_bounded(&acc_full[buf], (uint32_t)((n_it >> 1) & 1), abort);
@@ -499,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
         } else if (kEpi == kEpiDGlu) {
           epi_dglu(a, at, stage, lane, now, v);
         } else {
-          epi_linear(a, t.seg, at, stage, lane, now, v);
+          epi_linear(a, p, t.seg, at, stage, lane, now, v);
         }
       }
     }
@@ -515,16 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
   }
 }
 
-template __global__ void k_dense_gemm<kEpiLinear, false, false, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiLinear, false, true, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiLinear, true, true, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiGlu, false, false, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiDGlu, false, true, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiLinear, false, false, 2>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiLinear, false, true, 2>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiLinear, true, true, 2>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiGlu, false, false, 2>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiDGlu, false, true, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiLinear, 1>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiGlu, 1>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiDGlu, 1>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiLinear, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiGlu, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiDGlu, 2>(const __grid_constant__ DenseGemmArgs);
 
 size_t dense_gemm_smem_bytes() { return kRing + 4096 * kEpiWarps + 1024; }
 int dense_gemm_threads() { return kThreads; }

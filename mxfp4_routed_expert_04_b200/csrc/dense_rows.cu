@@ -19,8 +19,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kPrefetch = 16384;        // bytes of one L2 prefetch
-
 MOE_DEV void st_cluster4(uint32_t addr, const uint32_t* v) {
   asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};\n"
                ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
@@ -74,8 +72,8 @@ MOE_DEV void store_lanes8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, 
   const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
   const uint32_t code = e4m3_scale_code(m);
   if (!on) return;
-  static_cast<uint8_t*>(q)[(size_t)row * a.N + c] = (uint8_t)(e4m3_pair(v * e4m3_inv_scale(code), 0.0f) & 0xFFu);
-  if (lane == 0) s[(size_t)row * ((a.N + 31) / 32) + c / 32] = (uint8_t)code;
+  static_cast<uint8_t*>(q)[(size_t)row * a.p[0].N + c] = (uint8_t)(e4m3_pair(v * e4m3_inv_scale(code), 0.0f) & 0xFFu);
+  if (lane == 0) s[(size_t)row * ((a.p[0].N + 31) / 32) + c / 32] = (uint8_t)code;
 }
 // one held by eight neighbouring lanes, 4 columns each
 MOE_DEV void store_quads8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, int c, const float (&v)[4], bool on) {
@@ -87,8 +85,8 @@ MOE_DEV void store_quads8(const DenseGemmArgs& a, void* q, uint8_t* s, int row, 
   for (int x = 1; x < 8; x <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
   const uint32_t code = e4m3_scale_code(m);
   if (!on) return;
-  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(q) + (size_t)row * a.N + c) = e4m3_quad(v, e4m3_inv_scale(code));
-  if (c % 32 == 0) s[(size_t)row * ((a.N + 31) / 32) + c / 32] = (uint8_t)code;
+  *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(q) + (size_t)row * a.p[0].N + c) = e4m3_quad(v, e4m3_inv_scale(code));
+  if (c % 32 == 0) s[(size_t)row * ((a.p[0].N + 31) / 32) + c / 32] = (uint8_t)code;
 }
 MOE_DEV uint2 load4(const void* base, size_t off) {
   return *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + off);
@@ -110,12 +108,12 @@ MOE_DEV void add4(int f16, uint2 w, float (&v)[4]) {
 template <int kEpi>
 MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int rank, int S, int warp, int lane) {
   constexpr int kPer = (kEpi == kEpiGlu ? 64 : 128) / 4;
-  const int groups = a.M * kPer;
+  const int groups = a.p[0].M * kPer;
   for (int b = 32 * (rank * (kRowsThreads / 32) + warp); b < groups; b += S * kRowsThreads) {
     const int i = b + lane, t = i / kPer, m = 4 * (i - t * kPer), c = n0 + m;
-    const bool on = i < groups && c < a.N;
+    const bool on = i < groups && c < a.p[0].N;
     const uint32_t off = on ? (uint32_t)((t * 128 + m) * 4) : 0u;
-    const size_t o = (size_t)t * a.N + c;
+    const size_t o = (size_t)t * a.p[0].N + c;
     float v[4];
     if (kEpi == kEpiGlu) {
       float u[4];
@@ -130,9 +128,10 @@ MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int 
           store4(a.g, o, a.f16, v);
           store4(a.u, o, a.f16, u);
         }
+        fn_values(a.fn, v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = fn_value(a.fn, v[k]) * u[k];
-        store4(a.out[0], o, a.f16, v);
+        for (int k = 0; k < 4; ++k) v[k] *= u[k];
+        store4(a.p[0].out[0], o, a.f16, v);
       }
     } else {
       uint2 bias = make_uint2(0u, 0u), res = bias;
@@ -142,14 +141,11 @@ MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int 
       if (on) {
         if (a.bias) add4(a.f16, bias, v);
         if (a.pre) store4(a.pre, o, a.f16, v);
-        if (a.fn) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) v[k] = fn_value(a.fn, v[k]);
-        }
+        fn_values(a.fn, v);
         if (a.residual) add4(a.f16, res, v);
-        const size_t y = (size_t)t * a.ldo + c;
-        if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.out[0]) + y) = make_float4(v[0], v[1], v[2], v[3]);
-        else store4(a.out[0], y, a.f16, v);
+        const size_t y = (size_t)t * a.p[0].ldo + c;
+        if (a.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(a.p[0].out[0]) + y) = make_float4(v[0], v[1], v[2], v[3]);
+        else store4(a.p[0].out[0], y, a.f16, v);
       }
     }
   }
@@ -160,6 +156,7 @@ MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int 
 template <int kEpi>
 __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_constant__ DenseRowsArgs p) {
   const DenseGemmArgs& a = p.g;
+  const DenseProblem& b = a.p[0];
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -175,12 +172,12 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   const int stage_bytes = dense_rows_stage(tn);
   const int S = p.splits, rank = (int)blockIdx.x % S;
   const int n0 = (int)blockIdx.x / S * kRows;
-  const int ks = (a.K + 63) / 64;
+  const int ks = (b.K + 63) / 64;
   const int j0 = (int)((long)ks * rank / S), j1 = (int)((long)ks * (rank + 1) / S);
   const uint32_t tcols = tn <= 32 ? 32u : 64u;
   // pushed: units of 4 tokens x 32 rows, [unit slot][rank][kUnit] of 4 tokens of a
   // row, behind the ring; kept: floats [token][128 rows], over it
-  const bool push = a.M <= kRowsPush;
+  const bool push = b.M <= kRowsPush;
   float4* parts = reinterpret_cast<float4*>(smem + (push ? nst * stage_bytes : 0));
 
   if (threadIdx.x == 0) {
@@ -206,14 +203,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
         uint8_t* st = smem + s * stage_bytes;
         mbar_expect_tx(&full[s], (uint32_t)stage_bytes);
         if (kEpi == kEpiGlu) {
-          tc::tma_load_2d(st, &a.map_a[0], 64 * j, n0, &full[s]);
-          tc::tma_load_2d(st + 8192, &a.map_a[1], 64 * j, n0, &full[s]);
+          tc::tma_load_2d(st, &b.map_a[0], 64 * j, n0, &full[s]);
+          tc::tma_load_2d(st + 8192, &b.map_a[1], 64 * j, n0, &full[s]);
         } else {
-          tc::tma_load_2d(st, &a.map_a[0], 64 * j, n0, &full[s]);
+          tc::tma_load_2d(st, &b.map_a[0], 64 * j, n0, &full[s]);
         }
       };
       auto load_x = [&](int s, int j) {
-        tc::tma_load_2d(smem + s * stage_bytes + 16384, &a.map_b[0], 64 * j, 0, &full[s]);
+        tc::tma_load_2d(smem + s * stage_bytes + 16384, &b.map_b[0], 64 * j, 0, &full[s]);
       };
       if (!p.early) pdl_wait();
       const int pre = min(nst, j1 - j0);
@@ -228,15 +225,6 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
         load_w(s, j);
         load_x(s, j);
         if (++s == nst) { s = 0; ph ^= 1u; }
-      }
-      // its loads are all on their way: this CTA's share of what the next kernel
-      // of the stream reads goes to L2 meanwhile
-      if (ok && p.next_bytes) {
-        const uint64_t per_cta = (p.next_bytes + gridDim.x - 1) / gridDim.x;
-        const uint64_t per16 = (per_cta + 15) / 16 * 16;
-        const uint64_t lo = per16 * blockIdx.x, hi = min(lo + per16, p.next_bytes);
-        for (uint64_t o = lo; o < hi; o += kPrefetch)
-          tc::prefetch_l2(static_cast<const uint8_t*>(p.next) + o, (uint32_t)min((uint64_t)kPrefetch, hi - o));
       }
       if (!ok) {                        // let every issued copy land before the CTA can exit
         for (int i = 0; i < nst; ++i) mbar_wait(&full[i], i < s ? ph : ph ^ 1u, 1u << 14);
@@ -277,13 +265,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       tc::fence_after_sync();
       const uint32_t at = (uint32_t)(rank * kUnit + (kEpi == kEpiGlu ? 32 * (wq >> 1) : 0) + lane) * 16u;
       int slot = 0, owner = wq & (kPer - 1);        // of unit kPer * (token / 4) + this warp's rows
-      for (int c0 = 0; c0 < a.M; c0 += 16) {
+      for (int c0 = 0; c0 < b.M; c0 += 16) {
         uint32_t d[32];
         tc::ld_16cols(tbase + ((uint32_t)(32 * wq) << 16) + c0, d);
         tc::wait_ld();
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
-          if (c0 + i < a.M) {
+          if (c0 + i < b.M) {
             if (push) {
               while (owner >= S) { owner -= S; ++slot; }
               st_cluster4(tc::mapa(parts, (uint32_t)owner) + (uint32_t)(slot * S * kUnit * 16) + at, d + i);
@@ -303,15 +291,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   cluster_arrive();
   // pushed: this CTA's units (unit u is CTA u % S's), one a warp and turn; the
   // first one's inputs before the wait
-  const int units = push ? (a.M + 3) / 4 * kPer : 0;
+  const int units = push ? (b.M + 3) / 4 * kPer : 0;
   const int first = rank + S * warp, step = S * (kRowsThreads / 32);
   auto inputs = [&](int u, float& bias, float (&res)[4]) {
     const int t = u / kPer * 4, c = n0 + 32 * (u % kPer) + lane;
-    const bool on = kEpi == kEpiLinear && u < units && c < a.N;
+    const bool on = kEpi == kEpiLinear && u < units && c < b.N;
     bias = on && a.bias ? load16(a.f16, a.bias, (size_t)c) : 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      res[k] = on && a.residual && t + k < a.M ? load16(a.f16, a.residual, (size_t)(t + k) * a.ldr + c) : 0.0f;
+      res[k] = on && a.residual && t + k < b.M ? load16(a.f16, a.residual, (size_t)(t + k) * a.ldr + c) : 0.0f;
   };
   float bias, res[4];
   inputs(first, bias, res);
@@ -325,9 +313,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
     if (kEpi == kEpiGlu) sum_pushed(part + 32, S, kUnit, up);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (t + k >= a.M) break;                      // the same in every lane
-      const bool on = c < a.N;
-      const size_t o = (size_t)(t + k) * a.N + c;
+      if (t + k >= b.M) break;                      // the same in every lane
+      const bool on = c < b.N;
+      const size_t o = (size_t)(t + k) * b.N + c;
       if (kEpi == kEpiGlu) {
         if (a.g && a.saved8) {
           store_lanes8(a, a.g, a.g_s, t + k, c, v[k], on, lane);
@@ -338,15 +326,18 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
             store16(a.g, o, a.f16, v[k]);
             store16(a.u, o, a.f16, up[k]);
           }
-          store16(a.out[0], o, a.f16, fn_value(a.fn, v[k]) * up[k]);
+          float h[1] = {v[k]};
+          fn_values(a.fn, h);
+          store16(b.out[0], o, a.f16, h[0] * up[k]);
         }
       } else {
-        const float z = v[k] + bias;
-        if (on && a.pre) store16(a.pre, o, a.f16, z);
-        const float y = fn_value(a.fn, z) + res[k];
+        float z[1] = {v[k] + bias};
+        if (on && a.pre) store16(a.pre, o, a.f16, z[0]);
+        fn_values(a.fn, z);
+        const float y = z[0] + res[k];
         if (on) {
-          if (a.out_f32) static_cast<float*>(a.out[0])[(size_t)(t + k) * a.ldo + c] = y;
-          else store16(a.out[0], (size_t)(t + k) * a.ldo + c, a.f16, y);
+          if (a.out_f32) static_cast<float*>(b.out[0])[(size_t)(t + k) * b.ldo + c] = y;
+          else store16(b.out[0], (size_t)(t + k) * b.ldo + c, a.f16, y);
         }
       }
     }
