@@ -56,7 +56,7 @@ struct DenseGemmArgs {
   int32_t* status;
 };
 
-template <int kEpi, int kCg>
+template <int kEpi, int kCg, bool kPieces>
 __global__ void k_dense_gemm(const __grid_constant__ DenseGemmArgs a);
 size_t dense_gemm_smem_bytes();
 int dense_gemm_threads();
@@ -113,9 +113,10 @@ struct Ckpt8Args {
   uint8_t* s;
   int64_t rows, ld;         // ld: row pitch of the 16-bit side, in elements
   int cols, f16;
+  int width;                // 8-element groups of a block's row, a power of two in [4, kCkptThreads]
 };
 __global__ void k_ckpt8_pack(Ckpt8Args a);
 __global__ void k_ckpt8_unpack(Ckpt8Args a);
-constexpr int kCkptThreads = 256, kCkptSpan = 4 * kCkptThreads;   // groups of 8 elements a block takes at a time
+constexpr int kCkptThreads = 256, kCkptRows = 4;    // threads of a block; rows of a thread
 
 }  // namespace moe

@@ -153,13 +153,13 @@ struct Device {
 std::mutex g_mu;
 Device g_dev[64];
 
-template <int kEpi>
+template <int kEpi, bool kPieces = false>
 cudaError_t allow_smem() {
   const int bytes = (int)moe::dense_gemm_smem_bytes();
-  const cudaError_t e = cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, 1>,
+  const cudaError_t e = cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, 1, kPieces>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   return e != cudaSuccess ? e
-                          : cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, 2>,
+                          : cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, 2, kPieces>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
@@ -173,6 +173,7 @@ moe_status device(const Device** out) {
     cudaError_t e = cudaDeviceGetAttribute(&s.num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear>();
     if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu>();
+    if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu, true>();
     if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu>();
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(moe::k_dense_rows<moe::kEpiLinear>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -343,7 +344,7 @@ moe_status place(Launch& l, const TileChoice& t, bool glu, long* tiles, const ch
   return MOE_OK;
 }
 
-template <int kEpi>
+template <int kEpi, bool kPieces = false>
 moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* what) {
   constexpr bool glu = kEpi == moe::kEpiGlu;
   moe::DenseGemmArgs& g = l.g;
@@ -366,15 +367,15 @@ moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* wha
         one.a[0][k] = l.a[i][k];
         one.b[0][k] = l.b[i][k];
       }
-      TRY(enqueue<kEpi>(dv, one, st, what));
+      TRY((enqueue<kEpi, kPieces>(dv, one, st, what)));
     }
     return MOE_OK;
   }
   TRY(place(l, t, glu, &tiles, what));
   g.balanced = g.problems > 1;
   const int ctas = (int)std::min<long>(tiles, slots) * t.cg;
-  return launch(what, t.cg == 2 ? moe::k_dense_gemm<kEpi, 2> : moe::k_dense_gemm<kEpi, 1>, dim3((unsigned)ctas),
-                moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), t.cg, st, g);
+  return launch(what, t.cg == 2 ? moe::k_dense_gemm<kEpi, 2, kPieces> : moe::k_dense_gemm<kEpi, 1, kPieces>,
+                dim3((unsigned)ctas), moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), t.cg, st, g);
 }
 
 // Few tokens: the weights' rows over clusters that split K, so that up to two
@@ -427,10 +428,12 @@ moe_status ckpt8(const Device& dv, bool pack, int f16, int64_t rows, int cols, c
                  uint8_t* q, uint8_t* s, cudaStream_t st) {
   moe::Ckpt8Args c;
   c.src = src; c.dst = dst; c.q = q; c.s = s; c.rows = rows; c.ld = ld; c.cols = cols; c.f16 = f16;
-  const int64_t spans = (rows * ((cols + 31) / 32 * 4) + moe::kCkptSpan - 1) / moe::kCkptSpan;
-  const int64_t blocks = std::min<int64_t>(spans, 1 << 20);
-  return launch(pack ? "checkpoint pack" : "checkpoint unpack", pack ? moe::k_ckpt8_pack : moe::k_ckpt8_unpack,
-                dim3((unsigned)blocks), moe::kCkptThreads, 0, 1, st, c);
+  const int groups = (cols + 31) / 32 * 4;
+  for (c.width = 4; c.width < groups && c.width < moe::kCkptThreads;) c.width *= 2;
+  const int64_t high = (int64_t)moe::kCkptThreads / c.width * moe::kCkptRows;
+  const dim3 grid((unsigned)((rows + high - 1) / high), (unsigned)((groups + c.width - 1) / c.width));
+  return launch(pack ? "checkpoint pack" : "checkpoint unpack", pack ? moe::k_ckpt8_pack : moe::k_ckpt8_unpack, grid,
+                moe::kCkptThreads, 0, 1, st, c);
 }
 
 moe_status check_ckpt8(int32_t dtype, int64_t rows, int32_t cols, const void* x, int64_t* ld, const void* q,
@@ -583,8 +586,10 @@ moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, cons
     l.g.g = saved->g; l.g.u = saved->u; l.g.g_s = saved->g_s; l.g.u_s = saved->u_s;
     l.g.saved8 = p.save == MOE_SAVE_8;
   }
-  TRY(p.T <= moe::kRowsTokens ? rows<moe::kEpiGlu>(*dv, l, false, st, "gate/up projection")
-                              : enqueue<moe::kEpiGlu>(*dv, l, st, "gate/up projection"));
+  const char* what = "gate/up projection";
+  if (p.T <= moe::kRowsTokens) TRY(rows<moe::kEpiGlu>(*dv, l, false, st, what));
+  else if (l.g.saved8) TRY((enqueue<moe::kEpiGlu, true>(*dv, l, st, what)));
+  else TRY(enqueue<moe::kEpiGlu>(*dv, l, st, what));
   if (saved && saved->x_q)
     TRY(ckpt8(*dv, true, p.f16, p.T, p.H, x, nullptr, p.ldx, saved->x_q, saved->x_s, st));
   return project(*dv, p.T, p.H, p.I, p.f16, MOE_FN_NONE, p.out_f32, h, p.I, wd, nullptr, residual, p.ldr, y, p.ldy,

@@ -88,24 +88,28 @@ __global__ void __launch_bounds__(256) k_colsum(const float* part, int chunks, i
 
 namespace {
 
-// Element groups of 8, rows padded to whole blocks of 4 groups: group i of a
-// span of kSpan belongs to thread i % kCkptThreads, so neighbouring lanes hold
-// neighbouring 16 bytes and four lanes a block.
-constexpr int kSpan = kCkptSpan, kPerThread = kSpan / kCkptThreads;
+// Groups of 8 elements. A block is `width` groups wide (a power of two, so the
+// four lanes of a scale's 32 elements are neighbours) and kCkptThreads / width
+// rows high; a thread keeps its column and takes kAhead rows, all loaded before
+// it works, so no index is divided (with a division per group the kernels were
+// bound by instructions: 4096 x 8192 packed in 24 us).
+constexpr int kAhead = kCkptRows;
 
 struct Place {
-  int64_t row;
-  int group;                // group of the row
-  bool on;
+  int64_t row;              // first row; the next ones `high` further on
+  int group, high;
 };
-// place of group i of the span that starts at group g0 of row row0
-MOE_DEV Place place_of(const Ckpt8Args& a, int64_t row0, int g0, int i, int per_row) {
-  const int g = g0 + i, dr = g / per_row;
+MOE_DEV Place place_of(const Ckpt8Args& a) {
   Place p;
-  p.row = row0 + dr;
-  p.group = g - dr * per_row;
-  p.on = p.row < a.rows && 8 * p.group < a.cols;
+  p.high = kCkptThreads / a.width;
+  p.row = (int64_t)blockIdx.x * (p.high * kAhead) + threadIdx.x / a.width;
+  p.group = (int)(blockIdx.y * a.width + (threadIdx.x & (a.width - 1)));
   return p;
+}
+MOE_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 }  // namespace
@@ -113,69 +117,63 @@ MOE_DEV Place place_of(const Ckpt8Args& a, int64_t row0, int g0, int i, int per_
 __global__ void __launch_bounds__(kCkptThreads) k_ckpt8_pack(Ckpt8Args a) {
   pdl_wait();
   pdl_trigger();
-  const int nb = (a.cols + 31) / 32, per_row = 4 * nb;
-  const int64_t total = a.rows * per_row;
-  for (int64_t base = (int64_t)blockIdx.x * kSpan; base < total; base += (int64_t)gridDim.x * kSpan) {
-    const int64_t row0 = base / per_row;
-    const int g0 = (int)(base - row0 * per_row);
-    Place p[kPerThread];
-    uint4 w[kPerThread];
+  const int nb = (a.cols + 31) / 32;
+  const Place p = place_of(a);
+  const bool in_row = 8 * p.group < a.cols;
+  uint4 w[kAhead];
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      p[k] = place_of(a, row0, g0, threadIdx.x + k * kCkptThreads, per_row);
-      w[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (p[k].on) w[k] = ldg_stream(static_cast<const uint16_t*>(a.src) + p[k].row * a.ld + 8 * p[k].group);
-    }
+  for (int k = 0; k < kAhead; ++k) {
+    const int64_t r = p.row + k * p.high;
+    w[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (in_row && r < a.rows) w[k] = ldg_stream(static_cast<const uint16_t*>(a.src) + r * a.ld + 8 * p.group);
+  }
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      float v[8];
-      unpack16x8(a.f16, w[k], v);
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const uint32_t code = e4m3_scale_code(m);
-      const float inv = e4m3_inv_scale(code);
-      if (!p[k].on) continue;
-      *reinterpret_cast<uint2*>(a.q + p[k].row * a.cols + 8 * p[k].group) =
-          make_uint2(e4m3_quad(v, inv), e4m3_quad(v + 4, inv));
-      if ((p[k].group & 3) == 0) a.s[p[k].row * nb + p[k].group / 4] = (uint8_t)code;
-    }
+  for (int k = 0; k < kAhead; ++k) {
+    // the largest magnitude as a 16-bit pattern: they grow with it, NaN above all
+    uint32_t m = max_u16x2(max_u16x2(w[k].x & 0x7FFF7FFFu, w[k].y & 0x7FFF7FFFu),
+                           max_u16x2(w[k].z & 0x7FFF7FFFu, w[k].w & 0x7FFF7FFFu));
+    m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max_u16x2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    float top, unused;
+    unpack16(a.f16, max(m & 0xFFFFu, m >> 16), top, unused);
+    const uint32_t code = e4m3_scale_code(__float_as_uint(top));
+    const float inv = e4m3_inv_scale(code);
+    float v[8];
+    unpack16x8(a.f16, w[k], v);
+    const int64_t r = p.row + k * p.high;
+    if (!in_row || r >= a.rows) continue;
+    *reinterpret_cast<uint2*>(a.q + r * a.cols + 8 * p.group) = make_uint2(e4m3_quad(v, inv), e4m3_quad(v + 4, inv));
+    if ((p.group & 3) == 0) a.s[r * nb + p.group / 4] = (uint8_t)code;
   }
 }
 
 __global__ void __launch_bounds__(kCkptThreads) k_ckpt8_unpack(Ckpt8Args a) {
   pdl_wait();
   pdl_trigger();
-  const int nb = (a.cols + 31) / 32, per_row = 4 * nb;
-  const int64_t total = a.rows * per_row;
-  for (int64_t base = (int64_t)blockIdx.x * kSpan; base < total; base += (int64_t)gridDim.x * kSpan) {
-    const int64_t row0 = base / per_row;
-    const int g0 = (int)(base - row0 * per_row);
-    Place p[kPerThread];
-    uint2 w[kPerThread];
-    uint32_t code[kPerThread];
+  const int nb = (a.cols + 31) / 32;
+  const Place p = place_of(a);
+  if (8 * p.group >= a.cols) return;
+  uint2 w[kAhead];
+  uint32_t code[kAhead];
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      p[k] = place_of(a, row0, g0, threadIdx.x + k * kCkptThreads, per_row);
-      w[k] = make_uint2(0u, 0u);
-      code[k] = 0u;
-      if (p[k].on) {
-        w[k] = __ldg(reinterpret_cast<const uint2*>(a.q + p[k].row * a.cols + 8 * p[k].group));
-        code[k] = __ldg(a.s + p[k].row * nb + p[k].group / 4);
-      }
+  for (int k = 0; k < kAhead; ++k) {
+    const int64_t r = p.row + k * p.high;
+    w[k] = make_uint2(0u, 0u);
+    code[k] = 0u;
+    if (r < a.rows) {
+      w[k] = __ldg(reinterpret_cast<const uint2*>(a.q + r * a.cols + 8 * p.group));
+      code[k] = __ldg(a.s + r * nb + p.group / 4);
     }
+  }
 #pragma unroll
-    for (int k = 0; k < kPerThread; ++k) {
-      if (!p[k].on) continue;
-      const float s = e8m0_to_f32(code[k]);
-      float v[8];
-      e4m3_unquad(w[k].x, s, v);
-      e4m3_unquad(w[k].y, s, v + 4);
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dst) + p[k].row * a.ld + 8 * p[k].group) =
-          pack16x8(a.f16, v);
-    }
+  for (int k = 0; k < kAhead; ++k) {
+    const int64_t r = p.row + k * p.high;
+    if (r >= a.rows) break;
+    const float s = e8m0_to_f32(code[k]);
+    float v[8];
+    e4m3_unquad(w[k].x, s, v);
+    e4m3_unquad(w[k].y, s, v + 4);
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dst) + r * a.ld + 8 * p.group) = pack16x8(a.f16, v);
   }
 }
 

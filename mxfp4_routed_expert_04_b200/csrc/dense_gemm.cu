@@ -38,6 +38,14 @@ constexpr int kGroupM = 8;                         // row tiles that share their
 struct Tile {
   int prob, seg, m0, n0;
 };
+// kPieces: pieces of a tile's stages, at most 16 (K = 1024) each, that get
+// accumulators of their own and are added up in registers. A tensor-core sum
+// is cut off towards zero at every step of 16 k and loses about 1.5e-8 of
+// itself each time (random signs; measured 7.8e-6 at K = 8192, fp32 FMAs 0). In
+// 16-bit outputs that is nothing, but an 8-bit checkpoint moves a value that
+// lies so close to a border of its grid by a whole step: 3.3e-4 of the codes in
+// one piece of K = 8192, 8e-5 in pieces of 2048.
+MOE_DEV int pieces_of(int stages) { return (stages + 15) / 16; }
 // f(a_mn, b_mn) as compile-time constants: the directions that the launches use
 template <int kEpi, typename F>
 MOE_DEV void by_direction(const DenseProblem& p, F&& f) {
@@ -313,7 +321,7 @@ MOE_DEV void epi_dglu(const DenseGemmArgs& a, const EpiPos& e, uint32_t buf, int
   flush16(a, e, ga, lane, a.pre, e.N);
 }
 
-template <int kEpi, int kCg>
+template <int kEpi, int kCg, bool kPieces>
 __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constant__ DenseGemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -466,28 +474,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
       int s = 0, n_it = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int q = q0; q < q1 && ok; q += dq, ++n_it) {
+      for (int q = q0; q < q1 && ok; q += dq) {
         const DenseProblem& p = a.p[tile_of(q).prob];
         const int ks = stages_of(p);
-        const int buf = n_it & 1;
-        const uint32_t acc_ph = (uint32_t)((n_it >> 1) & 1);
-        if (!tc::wait_bounded<(kCg > 1)>(&acc_empty[buf], acc_ph ^ 1u, abort)) break;
-        tc::fence_after_sync();
-        const uint32_t d = tbase + 256u * buf;
         auto issue = [&](auto a_mn, auto b_mn) {
           const uint32_t idesc = tc::idesc_16(a.f16, 128 * kCg, tn, a_mn, b_mn);
           constexpr uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
-          for (int j = 0; j < ks; ++j) {
-            if (!tc::wait_bounded(&full[s], ph, abort)) { ok = false; break; }
-            const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kATile;
-            const uint64_t da = a_mn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa);
-            const uint64_t db = b_mn ? tc::desc_mn_sw128(sb, 8192) : tc::desc_sw128(sb);
+          const int pieces = kPieces ? pieces_of(ks) : 1;
+          for (int i = 0; i < pieces && ok; ++i, ++n_it) {
+            const int buf = n_it & 1;
+            const int j0 = kPieces ? ks * i / pieces : 0, j1 = kPieces ? ks * (i + 1) / pieces : ks;
+            if (!tc::wait_bounded<(kCg > 1)>(&acc_empty[buf], (uint32_t)((n_it >> 1) & 1) ^ 1u, abort)) {
+              ok = false;
+              break;
+            }
+            tc::fence_after_sync();
+            const uint32_t d = tbase + 256u * buf;
+            for (int j = j0; j < j1; ++j) {
+              if (!tc::wait_bounded(&full[s], ph, abort)) { ok = false; break; }
+              const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kATile;
+              const uint64_t da = a_mn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa);
+              const uint64_t db = b_mn ? tc::desc_mn_sw128(sb, 8192) : tc::desc_sw128(sb);
 #pragma unroll
-            for (int kb = 0; kb < 4; ++kb)                    // K = 16 per MMA
-              tc::mma_16<kCg>(d, da + kb * a_step, db + kb * b_step, idesc, (j > 0 || kb > 0) ? 1u : 0u);
-            tc::commit_cg<kCg>(&empty[s]);
-            if (j == ks - 1) tc::commit_cg<kCg>(&acc_full[buf]);
-            if (++s == nst) { s = 0; ph ^= 1u; }
+              for (int kb = 0; kb < 4; ++kb)                  // K = 16 per MMA
+                tc::mma_16<kCg>(d, da + kb * a_step, db + kb * b_step, idesc, (j > j0 || kb > 0) ? 1u : 0u);
+              tc::commit_cg<kCg>(&empty[s]);
+              if (j == j1 - 1) tc::commit_cg<kCg>(&acc_full[buf]);
+              if (++s == nst) { s = 0; ph ^= 1u; }
+            }
           }
         };
         by_direction<kEpi>(p, issue);
@@ -505,51 +519,85 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
     const uint32_t lane_off = (uint32_t)(32 * wq) << 16;
     const uint32_t stage = smem_u32(smem + kRing) + 4096u * (uint32_t)(warp - 2);
     int n_it = 0;
-    for (int q = q0; q < q1; q += dq, ++n_it) {
+    // the accumulators of turn n_it are complete; they are handed back by release()
+    auto ready = [&]() {
+      const bool ok = tc::wait_bounded(&acc_full[n_it & 1], (uint32_t)((n_it >> 1) & 1), abort);
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+      tc::fence_after_sync();
+      return true;
+    };
+    auto release = [&]() {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (kCg == 1) tc::mbar_arrive(&acc_empty[n_it & 1]);
+        else tc::arrive_cluster(tc::mapa(&acc_empty[n_it & 1], 0));
+      }
+    };
+    bool ok = true;
+    for (int q = q0; q < q1 && ok; q += dq) {
       const Tile t = tile_of(q);
       const DenseProblem& p = a.p[t.prob];
-      const int buf = n_it & 1;
       EpiPos e = {t.m0 + 32 * wq, t.n0 + cfirst, p.M, p.N};
-      EpiIn in;
-      if (cfirst < cols) epi_fetch<kEpi>(a, e, lane, in);
-      const bool ok = tc::wait_bounded(&acc_full[buf], (uint32_t)((n_it >> 1) & 1), abort);
-      if (!__all_sync(0xFFFFFFFFu, ok)) break;
-      tc::fence_after_sync();
-      const uint32_t dcol = tbase + lane_off + 256u * buf;
-      auto release = [&]() {            // accumulators read: the MMA may reuse them
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) {
-          if (kCg == 1) tc::mbar_arrive(&acc_empty[buf]);
-          else tc::arrive_cluster(tc::mapa(&acc_empty[buf], 0));
+      if constexpr (kPieces) {
+        // this warp's columns, at most two blocks of 32, added up over the pieces
+        float g[2][32], u[2][32];
+        const int pieces = pieces_of(stages_of(p));
+        for (int i = 0; i < pieces; ++i, ++n_it) {
+          if (!(ok = ready())) break;
+          const uint32_t dcol = tbase + lane_off + 256u * (n_it & 1);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int c0 = cfirst + 64 * c;
+            if (c0 < cols) {
+              uint32_t d[32], d2[32];
+              tc::ld_32cols(dcol + c0, d);
+              tc::ld_32cols(dcol + cols + c0, d2);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                g[c][k] = __uint_as_float(d[k]) + (i ? g[c][k] : 0.0f);
+                u[c][k] = __uint_as_float(d2[k]) + (i ? u[c][k] : 0.0f);
+              }
+            }
+          }
+          release();
         }
-      };
-      if (cfirst >= cols) release();
-      for (int c0 = cfirst; c0 < cols; c0 += 64) {
-        uint32_t d[32], d2[32];
-        tc::ld_32cols(dcol + c0, d);
-        if (kEpi == kEpiGlu) tc::ld_32cols(dcol + cols + c0, d2);
-        const EpiIn now = in;
-        const EpiPos at = e;
-        if (kEpi != kEpiGlu && c0 + 64 < cols) {
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (cfirst + 64 * c < cols) epi_glu(a, e, stage, lane, g[c], u[c]);
           e.col += 64;
-          epi_fetch<kEpi>(a, e, lane, in);
-        } else {
+        }
+      } else {
+        EpiIn in;
+        if (cfirst < cols) epi_fetch<kEpi>(a, e, lane, in);
+        if (!(ok = ready())) break;
+        const uint32_t dcol = tbase + lane_off + 256u * (n_it & 1);
+        if (cfirst >= cols) release();
+        for (int c0 = cfirst; c0 < cols; c0 += 64) {
+          uint32_t d[32], d2[32];
+          tc::ld_32cols(dcol + c0, d);
+          if (kEpi == kEpiGlu) tc::ld_32cols(dcol + cols + c0, d2);
+          const EpiIn now = in;
+          const EpiPos at = e;
           e.col += 64;
+          if (kEpi != kEpiGlu && c0 + 64 < cols) epi_fetch<kEpi>(a, e, lane, in);
+          tc::wait_ld();
+          if (c0 + 64 >= cols) release();
+          float v[32];
+          floats(d, v);
+          if (kEpi == kEpiGlu) {
+            float u[32];
+            floats(d2, u);
+            epi_glu(a, at, stage, lane, v, u);
+          } else if (kEpi == kEpiDGlu) {
+            epi_dglu(a, at, stage, lane, now, v);
+          } else {
+            epi_linear(a, p, t.seg, at, stage, lane, now, v);
+          }
         }
-        tc::wait_ld();
-        if (c0 + 64 >= cols) release();
-        float v[32];
-        floats(d, v);
-        if (kEpi == kEpiGlu) {
-          float u[32];
-          floats(d2, u);
-          epi_glu(a, at, stage, lane, v, u);
-        } else if (kEpi == kEpiDGlu) {
-          epi_dglu(a, at, stage, lane, now, v);
-        } else {
-          epi_linear(a, p, t.seg, at, stage, lane, now, v);
-        }
+        ++n_it;
       }
     }
   }
@@ -564,12 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
   }
 }
 
-template __global__ void k_dense_gemm<kEpiLinear, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiGlu, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiDGlu, 1>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiLinear, 2>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiGlu, 2>(const __grid_constant__ DenseGemmArgs);
-template __global__ void k_dense_gemm<kEpiDGlu, 2>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiLinear, 1, false>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiGlu, 1, false>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiGlu, 1, true>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiDGlu, 1, false>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiLinear, 2, false>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiGlu, 2, false>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiGlu, 2, true>(const __grid_constant__ DenseGemmArgs);
+template __global__ void k_dense_gemm<kEpiDGlu, 2, false>(const __grid_constant__ DenseGemmArgs);
 
 size_t dense_gemm_smem_bytes() { return kRing + 4096 * kEpiWarps + 1024; }
 int dense_gemm_threads() { return kThreads; }
