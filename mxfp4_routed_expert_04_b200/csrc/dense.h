@@ -58,6 +58,12 @@ struct DenseGemmArgs {
 
 template <int kEpi, int kCg, bool kPieces>
 __global__ void k_dense_gemm(const __grid_constant__ DenseGemmArgs a);
+// small products: one tile of 128 rows and 64 or 128 columns per cluster of `splits` CTAs
+template <int kEpi>
+__global__ void k_dense_split(const __grid_constant__ DenseGemmArgs a, int splits, int stages);
+constexpr int kMaxSplits = 8, kSplitStages = 8;
+constexpr int kSplitRingShared = 108 * 1024, kSplitRingAlone = 196 * 1024;   // two CTAs an SM, one
+int dense_split_threads();
 size_t dense_gemm_smem_bytes();
 int dense_gemm_threads();
 

@@ -45,6 +45,7 @@ char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
   } while (0)
 
 constexpr size_t kStatusBytes = 256;
+constexpr int kPieceStages = 16;    // longest sum in front of an 8-bit checkpoint (K = 1024)
 
 moe_status check_width(const char* name, int v) {
   if (v < 8 || v > 65536 || v % 8 != 0)
@@ -153,6 +154,11 @@ struct Device {
 std::mutex g_mu;
 Device g_dev[64];
 
+template <int kEpi>
+cudaError_t allow_split() {
+  return cudaFuncSetAttribute(moe::k_dense_split<kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              moe::kSplitRingAlone + 1024);
+}
 template <int kEpi, bool kPieces = false>
 cudaError_t allow_smem() {
   const int bytes = (int)moe::dense_gemm_smem_bytes();
@@ -173,6 +179,9 @@ moe_status device(const Device** out) {
     cudaError_t e = cudaDeviceGetAttribute(&s.num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = allow_smem<moe::kEpiLinear>();
     if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu>();
+    if (e == cudaSuccess) e = allow_split<moe::kEpiLinear>();
+    if (e == cudaSuccess) e = allow_split<moe::kEpiGlu>();
+    if (e == cudaSuccess) e = allow_split<moe::kEpiDGlu>();
     if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu, true>();
     if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu>();
     if (e == cudaSuccess)
@@ -272,6 +281,26 @@ struct Launch {
     for (int k = 0; k < bn; ++k) b[i][k] = bm[k];
     return p;
   }
+  // problem i as a launch of its own
+  Launch only(int i) const {
+    Launch l = *this;
+    l.g.problems = 0;
+    l.copy(*this, i);
+    return l;
+  }
+  void take(const Launch& one) { copy(one, 0); }
+
+ private:
+  void copy(const Launch& from, int i) {
+    const int to = g.problems++;
+    g.p[to] = from.g.p[i];
+    na[to] = from.na[i];
+    nb[to] = from.nb[i];
+    for (int k = 0; k < 2; ++k) {
+      a[to][k] = from.a[i][k];
+      b[to][k] = from.b[i][k];
+    }
+  }
 };
 
 // Tile of a launch: a pair's 256 rows or one CTA's 128, and the columns, from
@@ -344,38 +373,86 @@ moe_status place(Launch& l, const TileChoice& t, bool glu, long* tiles, const ch
   return MOE_OK;
 }
 
+// A product whose tiles leave SMs idle and are long: one tile a cluster, its K
+// divided (k_dense_split). Times in us, fitted to both kernels at 18 shapes
+// from 80 x 1024 x 1024 to 2048 x 512 x 4096 (within 15%): the tiled kernel
+// takes 4.5 and 0.24 a stage; a cluster 5, 0.22 or 0.25 (64 or 128 columns) a
+// stage, 1.7 times that with two CTAs on an SM, and 0.4 for each CTA and 64
+// columns that are added up. (100 x 2048 x 8192: 36 us tiled, 13.5 in clusters
+// of 4; 512 x 512 x 8192: 31 and 14.)
+struct SplitChoice {
+  int n, splits;            // splits 0: the tiled kernel
+};
+SplitChoice pick_split(const Device& dv, const Launch& one, bool glu, bool grads, int longest_piece) {
+  SplitChoice best = {0, 0};
+  const moe::DenseProblem& p = one.g.p[0];
+  const TileChoice t = pick_tile(dv, one.g, glu);
+  if (tiles_of(p, t.cg, glu ? t.n / 2 : t.n) > dv.num_sms / t.cg) return best;    // more than a wave
+  const long ks = stages_of(p);
+  double best_us = 4.5 + 0.24 * ks;
+  if (grads) best_us *= 0.75;           // gradients share a launch otherwise, which is worth about a quarter
+  for (int n = 64; n <= 128; n *= 2) {
+    const long tiles = tiles_of(p, 1, glu ? n / 2 : n);
+    for (int s = 2; s <= moe::kMaxSplits && 2 * s <= ks && tiles * s <= 2L * dv.num_sms; ++s) {
+      if ((ks + s - 1) / s > longest_piece) continue;
+      const double stage = (n == 64 ? 0.22 : 0.25) * (tiles * s > dv.num_sms ? 1.7 : 1.0);
+      const double us = 5.0 + stage * ((ks + s - 1) / s) + 0.4 * s * (n / 64);
+      if (us < best_us) {
+        best_us = us;
+        best = {n, s};
+      }
+    }
+  }
+  return best;
+}
+template <int kEpi>
+moe_status split(const Device& dv, Launch& l, const SplitChoice& c, cudaStream_t st, const char* what) {
+  long tiles = 0;
+  TRY(place(l, {1, c.n}, kEpi == moe::kEpiGlu, &tiles, what));
+  // up to one CTA an SM: the ring takes the SM's memory, also so that clusters
+  // that start under the previous kernel do not gather, two CTAs an SM, on the
+  // SMs it leaves idle (a block's input gradient behind its hidden gradient at
+  // T = 777: 26 us, 15 by itself)
+  const int ring = tiles * c.splits <= dv.num_sms ? moe::kSplitRingAlone : moe::kSplitRingShared;
+  const int stages = std::min(moe::kSplitStages, ring / (128 * 128 + c.n * 128));
+  return launch(what, moe::k_dense_split<kEpi>, dim3((unsigned)(tiles * c.splits)), moe::dense_split_threads(),
+                (size_t)ring + 1024, c.splits, st, l.g, c.splits, stages);
+}
+
 template <int kEpi, bool kPieces = false>
 moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* what) {
   constexpr bool glu = kEpi == moe::kEpiGlu;
-  moe::DenseGemmArgs& g = l.g;
+  // whether a product is split goes by itself alone, so its results do not
+  // depend on which others are asked for
+  Launch rest = l;
+  rest.g.problems = 0;
+  for (int i = 0; i < l.g.problems; ++i) {
+    Launch one = l.only(i);
+    const SplitChoice c = pick_split(dv, one, glu, kEpi == moe::kEpiLinear && one.g.p[0].b_mn, kPieces ? kPieceStages : 1 << 30);
+    if (c.splits) TRY(split<kEpi>(dv, one, c, st, what));
+    else rest.take(one);
+  }
+  if (rest.g.problems == 0) return MOE_OK;
+  moe::DenseGemmArgs& g = rest.g;
   const TileChoice t = pick_tile(dv, g, glu);
   const long slots = dv.num_sms / t.cg;
   long tiles = 0;
-  for (int i = 0; i < g.problems; ++i) tiles += tiles_of(g.p[i], t.cg, t.n);
+  for (int i = 0; i < g.problems; ++i) tiles += tiles_of(g.p[i], t.cg, glu ? t.n / 2 : t.n);
   // Several products go in one launch, in equal shares of their stages, while
   // they are a few waves together; longer ones keep their own launches, whose
   // neighbouring tiles share operands in L2 (gradients at T = 777, 1000 x 1352:
   // 63 us in three launches, 49 in one; at 4096, 8192 x 2048: 682 and 691).
-  if (g.problems > 1 && tiles >= 4 * slots) {
-    for (int i = 0; i < g.problems; ++i) {
-      Launch one = l;
-      one.g.problems = 1;
-      one.g.p[0] = g.p[i];
-      one.na[0] = l.na[i];
-      one.nb[0] = l.nb[i];
-      for (int k = 0; k < 2; ++k) {
-        one.a[0][k] = l.a[i][k];
-        one.b[0][k] = l.b[i][k];
-      }
-      TRY((enqueue<kEpi, kPieces>(dv, one, st, what)));
-    }
-    return MOE_OK;
+  const bool together = g.problems == 1 || tiles < 4 * slots;
+  for (int i = 0; i < (together ? 1 : g.problems); ++i) {
+    Launch part = together ? rest : rest.only(i);
+    const TileChoice pt = together ? t : pick_tile(dv, part.g, glu);
+    TRY(place(part, pt, glu, &tiles, what));
+    part.g.balanced = part.g.problems > 1;
+    const int ctas = (int)std::min<long>(tiles, dv.num_sms / pt.cg) * pt.cg;
+    TRY(launch(what, pt.cg == 2 ? moe::k_dense_gemm<kEpi, 2, kPieces> : moe::k_dense_gemm<kEpi, 1, kPieces>,
+               dim3((unsigned)ctas), moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), pt.cg, st, part.g));
   }
-  TRY(place(l, t, glu, &tiles, what));
-  g.balanced = g.problems > 1;
-  const int ctas = (int)std::min<long>(tiles, slots) * t.cg;
-  return launch(what, t.cg == 2 ? moe::k_dense_gemm<kEpi, 2, kPieces> : moe::k_dense_gemm<kEpi, 1, kPieces>,
-                dim3((unsigned)ctas), moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), t.cg, st, g);
+  return MOE_OK;
 }
 
 // Few tokens: the weights' rows over clusters that split K, so that up to two

@@ -612,6 +612,231 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
   }
 }
 
+// --- small products ----------------------------------------------------------------
+// One tile of 128 rows a cluster, whose CTAs divide its stages: for a product
+// that leaves SMs idle in k_dense_gemm although its few tiles are long. Two
+// CTAs fit an SM where there are more than SMs, so a CTA's start and epilogue
+// run under its neighbour's products. The CTAs keep their fp32 sums in their
+// own shared memory, over the ring; behind a cluster barrier the 32 x 32 blocks
+// of the tile go to the cluster's warps, which add the CTAs' parts in rank
+// order (the same bits every run) and run the epilogue above.
+namespace {
+
+constexpr int kSplitWarps = 4;                     // epilogue warps: two CTAs' registers fit an SM
+constexpr int kSplitThreads = 64 + 32 * kSplitWarps;
+
+MOE_DEV float4 ld_cluster16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// byte offset of 16-byte chunk c of row r in the sums [128][tn] (no bank conflicts down a column)
+MOE_DEV uint32_t sum_at(int r, int c, int tn) { return (uint32_t)(r * tn * 4 + ((c ^ (r & 7)) << 4)); }
+// the cluster's sums of a block (rows r0.., columns col..) in the epilogue's
+// layout, one row a lane. Neighbouring lanes fetch neighbouring chunks (a lane
+// on its own row made 32 requests of each load) and rows change hands in `buf`.
+MOE_DEV void sum_block(const uint8_t* sums, int splits, int r0, int col, int tn, uint32_t buf, int lane,
+                       float (&v)[32]) {
+  const int r = lane >> 3, c = lane & 7;
+  float4 t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int k = 0; k < splits; ++k) {
+    const uint32_t base = tc::mapa(sums, (uint32_t)k);
+    float4 q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = ld_cluster16(base + sum_at(r0 + 4 * i + r, col / 4 + c, tn));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      t[i].x += q[i].x;
+      t[i].y += q[i].y;
+      t[i].z += q[i].z;
+      t[i].w += q[i].w;
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    sts16(stage128(buf, 4 * i + r, c), make_uint4(__float_as_uint(t[i].x), __float_as_uint(t[i].y),
+                                                  __float_as_uint(t[i].z), __float_as_uint(t[i].w)));
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint4 w = lds16(stage128(buf, lane, j));
+    v[4 * j] = __uint_as_float(w.x);
+    v[4 * j + 1] = __uint_as_float(w.y);
+    v[4 * j + 2] = __uint_as_float(w.z);
+    v[4 * j + 3] = __uint_as_float(w.w);
+  }
+}
+
+}  // namespace
+
+template <int kEpi>
+__global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_constant__ DenseGemmArgs a, int splits, int nst) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  __shared__ uint64_t full[kSplitStages], empty[kSplitStages], acc_full;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tn = a.tile_n, cols = kEpi == kEpiGlu ? tn / 2 : tn;
+  const int stage_bytes = kATile + tn * 128;
+  const int rank = (int)blockIdx.x % splits, q = (int)blockIdx.x / splits;
+
+  // the tile: column tiles of a row tile follow each other
+  int pi = 0;
+  while (pi + 1 < a.problems && q >= a.p[pi + 1].first) ++pi;
+  const DenseProblem& p = a.p[pi];
+  const int mt1 = (p.M + 127) / 128, nt = (p.N + cols - 1) / cols;
+  const int m = (q - p.first) / nt, seg = m / mt1;
+  const int m0 = (m - seg * mt1) * 128, n0 = (q - p.first - m * nt) * cols;
+  const int ks1 = (p.K + 63) / 64, ks = ks1 * p.k_segs;
+  const int j0 = (int)((long)ks * rank / splits), j1 = (int)((long)ks * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < nst; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&acc_full, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    tc::prefetch_map(&p.map_a[p.m_segs > 1 ? seg : 0]);
+    tc::prefetch_map(&p.map_b[0]);
+  }
+  if (warp == 1) tc::alloc_cg<1>(&tmem_slot, tn <= 64 ? 64u : 128u);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    if (tc::elect_one()) {
+      int s = 0, issued = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      auto fill = [&](auto a_mn, auto b_mn) {
+        for (int j = j0; j < j1; ++j) {
+          if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
+          uint8_t* sa = smem + s * stage_bytes;
+          uint8_t* sb = sa + kATile;
+          const int kseg = j >= ks1 ? 1 : 0, k0 = (j - kseg * ks1) * 64;
+          const CUtensorMap* ma = &p.map_a[p.m_segs > 1 ? seg : kseg];
+          const CUtensorMap* mb = &p.map_b[kseg];
+          mbar_expect_tx(&full[s], (uint32_t)stage_bytes);
+          if constexpr (a_mn) {
+            tc::tma_load_2d(sa, ma, m0, k0, &full[s]);
+            tc::tma_load_2d(sa + 8192, ma, m0 + 64, k0, &full[s]);
+          } else {
+            tc::tma_load_2d(sa, ma, k0, m0, &full[s]);
+          }
+          if constexpr (kEpi == kEpiGlu) {
+            tc::tma_load_2d(sb, &p.map_b[0], k0, n0, &full[s]);
+            tc::tma_load_2d(sb + cols * 128, &p.map_b[1], k0, n0, &full[s]);
+          } else if constexpr (b_mn) {
+            for (int i = 0; i < tn / 64; ++i) tc::tma_load_2d(sb + i * 8192, mb, n0 + 64 * i, k0, &full[s]);
+          } else {
+            tc::tma_load_2d(sb, mb, k0, n0, &full[s]);
+          }
+          ++issued;
+          if (++s == nst) { s = 0; ph ^= 1u; }
+        }
+      };
+      by_direction<kEpi>(p, fill);
+      if (!ok) {                        // let every issued copy land before the CTA can exit
+        for (int i = 0; i < nst && i < issued; ++i) mbar_wait(&full[i], (uint32_t)((issued - 1 - i) / nst & 1), 1u << 14);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    if (tc::elect_one()) {
+      int s = 0;
+      uint32_t ph = 0;
+      auto issue = [&](auto a_mn, auto b_mn) {
+        const uint32_t idesc = tc::idesc_16(a.f16, 128, tn, a_mn, b_mn);
+        constexpr uint32_t a_step = a_mn ? 2048 >> 4 : 32 >> 4, b_step = b_mn ? 2048 >> 4 : 32 >> 4;
+        for (int j = j0; j < j1; ++j) {
+          if (!tc::wait_bounded(&full[s], ph, abort)) break;
+          const uint32_t sa = smem_u32(smem + s * stage_bytes), sb = sa + kATile;
+          const uint64_t da = a_mn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa);
+          const uint64_t db = b_mn ? tc::desc_mn_sw128(sb, 8192) : tc::desc_sw128(sb);
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb)
+            tc::mma_16<1>(tbase, da + kb * a_step, db + kb * b_step, idesc, (j > j0 || kb > 0) ? 1u : 0u);
+          tc::commit_cg<1>(&empty[s]);
+          if (++s == nst) { s = 0; ph ^= 1u; }
+        }
+      };
+      by_direction<kEpi>(p, issue);
+      tc::commit_cg<1>(&acc_full);      // also when it gave up: no MMA may run past the CTA's exit
+    }
+    __syncwarp();
+  } else {
+    // ---------------- this CTA's sums, over the ring (warps 2-5) ----------------
+    const int wq = warp & 3;
+    const bool ok = tc::wait_bounded(&acc_full, 0, abort);
+    if (__all_sync(0xFFFFFFFFu, ok)) {
+      tc::fence_after_sync();
+      for (int c0 = 0; c0 < tn; c0 += 32) {
+        uint32_t d[32];
+        tc::ld_32cols(tbase + ((uint32_t)(32 * wq) << 16) + c0, d);
+        tc::wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          sts16(smem_u32(smem) + sum_at(32 * wq + lane, c0 / 4 + j, tn),
+                make_uint4(d[4 * j], d[4 * j + 1], d[4 * j + 2], d[4 * j + 3]));
+      }
+    }
+    __syncwarp();
+  }
+  tc::fence_before_sync();
+  if (splits > 1) tc::cluster_sync();
+  else __syncthreads();
+  if (warp >= 2) {
+    // ---------------- the tile's 32 x 32 blocks, dealt to the cluster's warps ----------------
+    const uint32_t stage = smem_u32(smem + 128 * tn * 4) + 4096u * (uint32_t)(warp - 2);
+    const int blocks = 4 * (cols / 32);
+    for (int b = rank + splits * (warp - 2); b < blocks; b += splits * kSplitWarps) {
+      const int r0 = 32 * (b & 3), c0 = 32 * (b >> 2);
+      const EpiPos e = {m0 + r0, n0 + c0, p.M, p.N};
+      if (e.row >= p.M || e.col >= p.N) continue;
+      EpiIn in;
+      epi_fetch<kEpi>(a, e, lane, in);
+      float v[32];
+      sum_block(smem, splits, r0, c0, tn, stage, lane, v);
+      if constexpr (kEpi == kEpiGlu) {
+        float u[32];
+        sum_block(smem, splits, r0, cols + c0, tn, stage, lane, u);
+        epi_glu(a, e, stage, lane, v, u);
+      } else if constexpr (kEpi == kEpiDGlu) {
+        epi_dglu(a, e, stage, lane, in, v);
+      } else {
+        epi_linear(a, p, seg, e, stage, lane, in, v);
+      }
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort) atomicOr(a.status, kStatusWaitTimeout);
+  if (splits > 1) tc::cluster_sync();   // the other CTAs read this one's sums
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, tn <= 64 ? 64u : 128u);
+  }
+}
+
+template __global__ void k_dense_split<kEpiLinear>(const __grid_constant__ DenseGemmArgs, int, int);
+template __global__ void k_dense_split<kEpiGlu>(const __grid_constant__ DenseGemmArgs, int, int);
+template __global__ void k_dense_split<kEpiDGlu>(const __grid_constant__ DenseGemmArgs, int, int);
+int dense_split_threads() { return kSplitThreads; }
+
 template __global__ void k_dense_gemm<kEpiLinear, 1, false>(const __grid_constant__ DenseGemmArgs);
 template __global__ void k_dense_gemm<kEpiGlu, 1, false>(const __grid_constant__ DenseGemmArgs);
 template __global__ void k_dense_gemm<kEpiGlu, 1, true>(const __grid_constant__ DenseGemmArgs);

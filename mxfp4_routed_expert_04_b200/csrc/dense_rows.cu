@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
     pdl_wait();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
+    pdl_wait();                         // its bounded waits begin when the tokens can arrive
     if (tc::elect_one()) {
       const uint32_t idesc = tc::idesc_16(a.f16, 128, tn, false, false);
       int s = 0;
@@ -251,7 +252,6 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       tc::commit_cg<1>(&acc_full);      // also when it gave up: no MMA may run past the CTA's exit
     }
     __syncwarp();
-    pdl_wait();
   } else {
     // ---------------- partial sums to shared memory (warps 2-5) ----------------
     pdl_wait();

@@ -65,6 +65,12 @@ LINEAR = [
     (333, 1000, 776, HF, "gelu", True, False, False),
     (700, 2312, 136, BF, "none", True, True, False),
     (1031, 1288, 328, HF, "none", False, True, False),
+    # few and long tiles: K divided over clusters
+    (66, 264, 4096, BF, "none", True, True, False),
+    (100, 1024, 8192, BF, "silu", True, False, False),
+    (129, 520, 5000, HF, "gelu", True, True, True),
+    (300, 200, 4104, BF, "none", False, True, False),
+    (1000, 512, 2048, BF, "relu", True, True, False),
 ]
 
 
@@ -208,6 +214,10 @@ FFN = [
     (130, 1000, 200, BF, "gelu", False, False),
     (300, 392, 712, HF, "silu", True, False),
     (520, 256, 384, BF, "relu", True, False),
+    # long sums: K divided over clusters, or (8-bit checkpoints) in pieces
+    (70, 4096, 264, BF, "silu", True, False),
+    (200, 2504, 328, HF, "gelu", False, False),
+    (1100, 2248, 1544, BF, "silu", True, False),
 ]
 
 
@@ -486,10 +496,33 @@ def test_calls_on_a_stream_of_their_own():
     R.check(y, R.ffn(x, wg, wu, wd, None, "silu", dt, dt)[0], "y", 2, dt)
 
 
+def test_calls_on_two_streams_at_once():
+    """Separate workspaces and outputs, the same inputs: the results of one call at a time."""
+    H, I, dt = 520, 1032, BF
+    for T in (1, 30, 100, 400):
+        x, wg, wu, wd = ffn_tensors(T, H, I, dt)
+        d = M.MoeFfnDims(T=T, H=H, I=I, fn=1, save=M.SAVE_8)
+        runs = []
+        for _ in range(2):
+            saved, got = M.FfnSaved(d), ffn_buffers(T, H, I, dt)
+            runs.append((torch.cuda.Stream(), workspace(M.moe_ffn_workspace_size(d)), saved, empty((T, H), dt), got))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, ws, saved, y, got in runs:
+                M.moe_ffn(d, x, wg, wu, wd, None, y, saved, ws, stream=s)
+                M.moe_ffn_backward(d, y, None, wg, wu, wd, saved, got["dx"], got["dwg"], got["dwu"], got["dwd"], ws,
+                                   stream=s)
+        torch.cuda.synchronize()
+        R.check(runs[0][3], R.ffn(x, wg, wu, wd, None, "silu", dt, dt)[0], "y", 2, dt)
+        assert torch.equal(runs[0][3], runs[1][3])
+        for n in runs[0][4]:
+            assert torch.equal(runs[0][4][n], runs[1][4][n]), n
+
+
 def test_one_output_feeds_the_next_call_as_its_weight():
     """Back to back on one stream, the second reading the first's output as weights."""
     dt = BF
-    for T in (3, 200):
+    for T in (3, 40, 90, 200):
         a, b, x = rand((256, 128), 0.3, dt, 1), rand((264, 128), 0.3, dt, 2), rand((T, 264), 1, dt, 3)
         w, y = empty((256, 264), dt), empty((T, 256), dt)
         d1, d2 = M.MoeLinearDims(T=256, N=264, K=128), M.MoeLinearDims(T=T, N=256, K=264)
