@@ -90,8 +90,8 @@ struct LinearPlan {
   int dz_rows, dz_chunks;       // row chunks of the bias gradient's partial sums
   size_t off_dz, off_part, total;
 };
-// rows of a bias-gradient chunk: at most 128 chunks, at least 64 rows each
-int dz_chunk_rows(int T) { return std::max(64, (T + 127) / 128); }
+// rows of a bias-gradient chunk: at most 128 chunks, at least 16 rows each
+int dz_chunk_rows(int T) { return std::max(16, (T + 127) / 128); }
 
 moe_status make_plan(const moe_linear_dims* d, LinearPlan& p) {
   if (!d) return fail(MOE_ERR_INVALID_ARG, "dims is NULL");

@@ -9,11 +9,11 @@ namespace moe {
 // blocks x row chunks. The column sums are added per row lane in row order,
 // then over the 8 lanes in order, then (k_colsum) over the chunks in order:
 // the same bits every run.
-__global__ void __launch_bounds__(kDzThreads) k_dz(DzArgs a) {
+__global__ void __launch_bounds__(kDzThreads, 4) k_dz(DzArgs a) {
   pdl_wait();
   pdl_trigger();
   __shared__ float red[8][kDzCols];
-  constexpr int kAhead = 4;               // rows a thread loads before it works
+  constexpr int kAhead = 2;               // rows a thread loads before it works
   const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int col = (int)blockIdx.x * kDzCols + 8 * cg;
   const int r0 = (int)blockIdx.y * a.rows, r1 = min(a.T, r0 + a.rows);
