@@ -309,6 +309,10 @@ struct Launch {
 // 4096 x 4096 x 8192, pairs of 256 / 192 / 160 / 128 columns 188 / 189 / 197 /
 // 213 us, single CTAs of 256 / 192 / 128 columns 218 / 223 / 257 us, which the
 // two lines below fit within 5%. MN-major B comes in boxes of 64 columns per CTA.
+// A pair also starts and ends later than a CTA: products of one wave are faster
+// on single CTAs up to about 25 stages (728 x 160 x 488: 6.0 us, pairs 6.7; at 128
+// stages 29 and 25).
+constexpr long kPairCost = 125000;
 struct TileChoice {
   int cg, n;
 };
@@ -341,7 +345,7 @@ TileChoice pick_tile(const Device& dv, const moe::DenseGemmArgs& g, bool glu) {
       // even share and the tile that ends it
       const long stages = g.problems == 1 ? (tiles + slots - 1) / slots * longest
                                           : std::max<long>(longest, (work + slots - 1) / slots + longest / 2);
-      const long cost = stages * (cg == 2 ? 100L * (n + 100) : 107L * (n + 136));
+      const long cost = cg == 2 ? stages * 100L * (n + 100) + kPairCost : stages * 107L * (n + 136);
       if (best_cost < 0 || cost < best_cost) {
         best_cost = cost;
         best = {cg, n};
