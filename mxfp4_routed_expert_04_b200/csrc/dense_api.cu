@@ -459,8 +459,12 @@ moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* wha
   return MOE_OK;
 }
 
-// Few tokens: the weights' rows over clusters that split K, so that up to two
-// CTAs of every SM stream (each at least four stages of 64 k).
+// Few tokens: the weights' rows over clusters that split K, down to two stages
+// of 64 k a CTA while there are fewer CTAs than SMs, four beyond (24 x 1024 ->
+// 1024: 3.9 us with 8 splits, 4.3 with 4; 24 x 1024 -> 4096: 6.4 with 8, 4.9
+// with 4). Above 32 tokens a K below 512 leaves nothing to split, and the tiled
+// kernel is faster (64 x 256 -> 256: 4.2 us and 5.9).
+bool few_tokens(int T, int K) { return T <= moe::kRowsTokens && (T <= 32 || K >= 512); }
 template <int kEpi>
 moe_status rows(const Device& dv, const Launch& l, bool early, cudaStream_t st, const char* what) {
   constexpr bool glu = kEpi == moe::kEpiGlu;
@@ -474,7 +478,8 @@ moe_status rows(const Device& dv, const Launch& l, bool early, cudaStream_t st, 
   for (int i = 0; i < (glu ? 2 : 1); ++i)
     TRY(map16(&p.map_a[i], w[i].p, r.g.f16, w[i].rows, w[i].cols, w[i].ld, glu ? 64 : 128, what));
   const int tile = glu ? 64 : 128, tiles = (p.N + tile - 1) / tile, ks = (p.K + 63) / 64;
-  r.splits = std::max(1, std::min(std::min(moe::kRowsSplits, 7 * dv.num_sms / 4 / tiles), ks / 4));
+  r.splits = std::max(std::min(dv.num_sms / tiles, ks / 2), std::min(7 * dv.num_sms / 4 / tiles, ks / 4));
+  r.splits = std::max(1, std::min(moe::kRowsSplits, r.splits));
   r.stages = moe::dense_rows_stages(p.M, r.g.tile_n);
   return launch(what, moe::k_dense_rows<kEpi>, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads,
                 moe::dense_rows_smem_bytes(), r.splits, st, r);
@@ -489,7 +494,7 @@ moe_status project(const Device& dv, int T, int N, int K, int f16, int fn, int o
   moe::DenseProblem& p = l.add(T, N, K, false, &a, 1, false, &b, 1);
   p.out[0] = y; p.ldo = ldy;
   l.g.fn = fn; l.g.out_f32 = out_f32; l.g.bias = bias; l.g.residual = residual; l.g.ldr = ldr; l.g.pre = pre;
-  return T <= moe::kRowsTokens ? rows<moe::kEpiLinear>(dv, l, early, st, what)
+  return few_tokens(T, K) ? rows<moe::kEpiLinear>(dv, l, early, st, what)
                                : enqueue<moe::kEpiLinear>(dv, l, st, what);
 }
 
@@ -668,7 +673,7 @@ moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, cons
     l.g.saved8 = p.save == MOE_SAVE_8;
   }
   const char* what = "gate/up projection";
-  if (p.T <= moe::kRowsTokens) TRY(rows<moe::kEpiGlu>(*dv, l, false, st, what));
+  if (few_tokens(p.T, p.H)) TRY(rows<moe::kEpiGlu>(*dv, l, false, st, what));
   else if (l.g.saved8) TRY((enqueue<moe::kEpiGlu, true>(*dv, l, st, what)));
   else TRY(enqueue<moe::kEpiGlu>(*dv, l, st, what));
   if (saved && saved->x_q)
