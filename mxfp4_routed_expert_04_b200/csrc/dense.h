@@ -103,7 +103,8 @@ struct DzArgs {
   const void* pre;
   void* dz;
   float* part;              // [chunks, N] or NULL
-  int T, N, rows, f16, fn;
+  void* db;                 // a single chunk: the sums themselves [N], or NULL
+  int T, N, rows, f16, fn, out_f32;
   int64_t lddy;
 };
 __global__ void k_dz(DzArgs a);

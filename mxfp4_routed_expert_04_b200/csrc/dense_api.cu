@@ -90,8 +90,9 @@ struct LinearPlan {
   int dz_rows, dz_chunks;       // row chunks of the bias gradient's partial sums
   size_t off_dz, off_part, total;
 };
-// rows of a bias-gradient chunk: at most 128 chunks, at least 16 rows each
-int dz_chunk_rows(int T) { return std::max(16, (T + 127) / 128); }
+// rows of a bias-gradient chunk: all of few tokens (no second kernel), else at
+// most 128 chunks of at least 16 rows
+int dz_chunk_rows(int T) { return T <= 64 ? T : std::max(16, (T + 127) / 128); }
 
 moe_status make_plan(const moe_linear_dims* d, LinearPlan& p) {
   if (!d) return fail(MOE_ERR_INVALID_ARG, "dims is NULL");
@@ -624,12 +625,15 @@ moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dy, cons
     moe::DzArgs z;
     z.dy = dy; z.pre = pre; z.lddy = p.ldy;
     z.dz = p.fn && (dx || dw) ? at(ws, p.off_dz) : nullptr;
-    z.part = dbias ? reinterpret_cast<float*>(at(ws, p.off_part)) : nullptr;
+    const bool one = p.dz_chunks == 1;
+    z.part = dbias && !one ? reinterpret_cast<float*>(at(ws, p.off_part)) : nullptr;
+    z.db = one ? dbias : nullptr;
+    z.out_f32 = p.out_f32;
     z.T = p.T; z.N = p.N; z.rows = p.dz_rows; z.f16 = p.f16; z.fn = p.fn;
     TRY(launch("activation gradient", moe::k_dz,
                dim3((unsigned)((p.N + moe::kDzCols - 1) / moe::kDzCols), (unsigned)p.dz_chunks), moe::kDzThreads, 0, 1,
                st, z));
-    if (dbias)
+    if (z.part)
       TRY(launch("bias gradient", moe::k_colsum, dim3((unsigned)((p.N + 31) / 32)), 256, 0, 1, st,
                  (const float*)z.part, p.dz_chunks, p.N, p.f16, p.out_f32, dbias));
     if (z.dz) dz = {z.dz, p.T, p.N, p.N};

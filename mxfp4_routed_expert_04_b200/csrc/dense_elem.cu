@@ -5,10 +5,15 @@
 
 namespace moe {
 
+MOE_DEV void store_sum(int f16, int out_f32, void* out, int c, float s) {
+  if (out_f32) static_cast<float*>(out)[c] = s;
+  else static_cast<uint16_t*>(out)[c] = (uint16_t)(pack16(f16, s, s) & 0xFFFFu);
+}
+
 // block: 32 column groups of 8 (256 columns) x 8 row lanes; grid: column
 // blocks x row chunks. The column sums are added per row lane in row order,
-// then over the 8 lanes in order, then (k_colsum) over the chunks in order:
-// the same bits every run.
+// then over the 8 lanes in order, then (k_colsum; not for a single chunk) over
+// the chunks in order: the same bits every run.
 __global__ void __launch_bounds__(kDzThreads, 4) k_dz(DzArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -51,7 +56,7 @@ __global__ void __launch_bounds__(kDzThreads, 4) k_dz(DzArgs a) {
       }
     }
   }
-  if (!a.part) return;
+  if (!a.part && !a.db) return;
 #pragma unroll
   for (int i = 0; i < 8; ++i) red[rl][8 * cg + i] = sum[i];
   __syncthreads();
@@ -60,7 +65,8 @@ __global__ void __launch_bounds__(kDzThreads, 4) k_dz(DzArgs a) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += red[i][threadIdx.x];
-    a.part[(size_t)blockIdx.y * a.N + c] = s;
+    if (a.db) store_sum(a.f16, a.out_f32, a.db, c, s);
+    else a.part[(size_t)blockIdx.y * a.N + c] = s;
   }
 }
 
@@ -82,8 +88,7 @@ __global__ void __launch_bounds__(256) k_colsum(const float* part, int chunks, i
   s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s += red[i][lane];
-  if (out_f32) static_cast<float*>(out)[c] = s;
-  else static_cast<uint16_t*>(out)[c] = (uint16_t)(pack16(f16, s, s) & 0xFFFFu);
+  store_sum(f16, out_f32, out, c, s);
 }
 
 namespace {
