@@ -151,6 +151,12 @@ moe_status make_plan(const moe_ffn_dims* d, FfnPlan& p) {
 struct Device {
   bool ready = false;
   int num_sms = 0;
+  // clusters of s CTAs that run at once with an SM for each CTA (the SMs of a GPC
+  // are not a multiple of every s: 45 of 3, 33 of 4, 15 of 8). The occupancy
+  // query counts one CTA an SM for kernels with tensor memory whatever they
+  // take; where memory and registers leave room for two, two run (seen from
+  // their SM numbers and times), so twice as many clusters.
+  int clusters[moe::kMaxSplits + 1] = {};
 };
 std::mutex g_mu;
 Device g_dev[64];
@@ -168,6 +174,26 @@ cudaError_t allow_smem() {
   return e != cudaSuccess ? e
                           : cudaFuncSetAttribute(moe::k_dense_gemm<kEpi, 2, kPieces>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename K>
+cudaError_t resident(K kernel, int threads, size_t smem, int (&out)[moe::kMaxSplits + 1]) {
+  for (int s = 1; s <= moe::kMaxSplits; ++s) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = s;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)s);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&out[s], kernel, &cfg);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 moe_status device(const Device** out) {
@@ -191,6 +217,9 @@ moe_status device(const Device** out) {
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(moe::k_dense_rows<moe::kEpiGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (int)moe::dense_rows_smem_bytes());
+    if (e == cudaSuccess)
+      e = resident(moe::k_dense_split<moe::kEpiLinear>, moe::dense_split_threads(), moe::kSplitRingAlone + 1024,
+                   s.clusters);
     if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "device setup: %s", cudaGetErrorString(e));
     s.ready = true;
   }
@@ -398,9 +427,9 @@ SplitChoice pick_split(const Device& dv, const Launch& one, bool glu, bool grads
   if (grads) best_us *= 0.75;           // gradients share a launch otherwise, which is worth about a quarter
   for (int n = 64; n <= 128; n *= 2) {
     const long tiles = tiles_of(p, 1, glu ? n / 2 : n);
-    for (int s = 2; s <= moe::kMaxSplits && 2 * s <= ks && tiles * s <= 2L * dv.num_sms; ++s) {
-      if ((ks + s - 1) / s > longest_piece) continue;
-      const double stage = (n == 64 ? 0.22 : 0.25) * (tiles * s > dv.num_sms ? 1.7 : 1.0);
+    for (int s = 2; s <= moe::kMaxSplits && 2 * s <= ks; ++s) {
+      if (tiles > 2 * dv.clusters[s] || (ks + s - 1) / s > longest_piece) continue;
+      const double stage = (n == 64 ? 0.22 : 0.25) * (tiles > dv.clusters[s] ? 1.7 : 1.0);
       const double us = 5.0 + stage * ((ks + s - 1) / s) + 0.4 * s * (n / 64);
       if (us < best_us) {
         best_us = us;
@@ -418,7 +447,7 @@ moe_status split(const Device& dv, Launch& l, const SplitChoice& c, cudaStream_t
   // that start under the previous kernel do not gather, two CTAs an SM, on the
   // SMs it leaves idle (a block's input gradient behind its hidden gradient at
   // T = 777: 26 us, 15 by itself)
-  const int ring = tiles * c.splits <= dv.num_sms ? moe::kSplitRingAlone : moe::kSplitRingShared;
+  const int ring = tiles <= dv.clusters[c.splits] ? moe::kSplitRingAlone : moe::kSplitRingShared;
   const int stages = std::min(moe::kSplitStages, ring / (128 * 128 + c.n * 128));
   return launch(what, moe::k_dense_split<kEpi>, dim3((unsigned)(tiles * c.splits)), moe::dense_split_threads(),
                 (size_t)ring + 1024, c.splits, st, l.g, c.splits, stages);
