@@ -92,7 +92,7 @@ constexpr int dense_rows_stages(int T, int tile_n) {
 static_assert(512 * kRowsTokens <= dense_rows_stage(16) * 2, "kept sums fit the ring's first two stages");
 constexpr int kDenseRowsStages = dense_rows_stages(16, 16);
 constexpr size_t dense_rows_smem_bytes() { return kRowsMemory + 1024; }
-template <int kEpi>
+template <int kEpi, bool kWMn>
 __global__ void k_dense_rows(const __grid_constant__ DenseRowsArgs a);
 
 // --- element kernels (dense_elem.cu) ------------------------------------------

@@ -45,6 +45,7 @@ char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
   } while (0)
 
 constexpr size_t kStatusBytes = 256;
+constexpr long kSmallWeights = 1 << 18;
 constexpr int kPieceStages = 16;    // longest sum in front of an 8-bit checkpoint (K = 1024)
 
 moe_status check_width(const char* name, int v) {
@@ -176,6 +177,11 @@ cudaError_t allow_smem() {
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+template <int kEpi, bool kWMn>
+cudaError_t allow_rows() {
+  return cudaFuncSetAttribute(moe::k_dense_rows<kEpi, kWMn>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)moe::dense_rows_smem_bytes());
+}
 template <typename K>
 cudaError_t resident(K kernel, int threads, size_t smem, int (&out)[moe::kMaxSplits + 1]) {
   for (int s = 1; s <= moe::kMaxSplits; ++s) {
@@ -211,12 +217,10 @@ moe_status device(const Device** out) {
     if (e == cudaSuccess) e = allow_split<moe::kEpiDGlu>();
     if (e == cudaSuccess) e = allow_smem<moe::kEpiGlu, true>();
     if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu>();
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(moe::k_dense_rows<moe::kEpiLinear>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)moe::dense_rows_smem_bytes());
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(moe::k_dense_rows<moe::kEpiGlu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)moe::dense_rows_smem_bytes());
+    if (e == cudaSuccess) e = allow_rows<moe::kEpiLinear, false>();
+    if (e == cudaSuccess) e = allow_rows<moe::kEpiGlu, false>();
+    if (e == cudaSuccess) e = allow_rows<moe::kEpiLinear, true>();
+    if (e == cudaSuccess) e = allow_rows<moe::kEpiDGlu, true>();
     if (e == cudaSuccess)
       e = resident(moe::k_dense_split<moe::kEpiLinear>, moe::dense_split_threads(), moe::kSplitRingAlone + 1024,
                    s.clusters);
@@ -453,6 +457,36 @@ moe_status split(const Device& dv, Launch& l, const SplitChoice& c, cudaStream_t
                 (size_t)ring + 1024, c.splits, st, l.g, c.splits, stages);
 }
 
+// Few tokens: the weights' rows over clusters that split K, down to two stages
+// of 64 k a CTA while there are fewer CTAs than SMs, four beyond (24 x 1024 ->
+// 1024: 3.9 us with 8 splits, 4.3 with 4; 24 x 1024 -> 4096: 6.4 with 8, 4.9
+// with 4). Above 32 tokens a K below 512 leaves nothing to split, and the tiled
+// kernel is faster (64 x 256 -> 256: 4.2 us and 5.9).
+bool few_tokens(int T, int K) { return T <= moe::kRowsTokens && (T <= 32 || K >= 512); }
+template <int kEpi, bool kWMn = false>
+moe_status rows(const Device& dv, const Launch& l, bool early, cudaStream_t st, const char* what) {
+  constexpr bool glu = kEpi == moe::kEpiGlu;
+  moe::DenseRowsArgs r;
+  r.g = l.g;
+  r.early = early;
+  moe::DenseProblem& p = r.g.p[0];
+  r.g.tile_n = (p.M + 15) / 16 * 16;
+  for (int i = 0; i < l.na[0]; ++i) {
+    const Mat& x = l.a[0][i];
+    TRY(map16(&p.map_b[i], x.p, r.g.f16, x.rows, x.cols, x.ld, r.g.tile_n, what));
+  }
+  for (int i = 0; i < l.nb[0]; ++i) {
+    const Mat& w = l.b[0][i];
+    TRY(map16(&p.map_a[i], w.p, r.g.f16, w.rows, w.cols, w.ld, glu || kWMn ? 64 : 128, what));
+  }
+  const int tile = glu ? 64 : 128, tiles = (p.N + tile - 1) / tile, ks = (int)stages_of(p);
+  r.splits = std::max(std::min(dv.num_sms / tiles, ks / 2), std::min(7 * dv.num_sms / 4 / tiles, ks / 4));
+  r.splits = std::max(1, std::min(moe::kRowsSplits, r.splits));
+  r.stages = moe::dense_rows_stages(p.M, r.g.tile_n);
+  return launch(what, moe::k_dense_rows<kEpi, kWMn>, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads,
+                moe::dense_rows_smem_bytes(), r.splits, st, r);
+}
+
 template <int kEpi, bool kPieces = false>
 moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* what) {
   constexpr bool glu = kEpi == moe::kEpiGlu;
@@ -462,7 +496,18 @@ moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* wha
   rest.g.problems = 0;
   for (int i = 0; i < l.g.problems; ++i) {
     Launch one = l.only(i);
-    const SplitChoice c = pick_split(dv, one, glu, kEpi == moe::kEpiLinear && one.g.p[0].b_mn, kPieces ? kPieceStages : 1 << 30);
+    const moe::DenseProblem& p = one.g.p[0];
+    // dX and the hidden gradient of few tokens; a small dX stays in the launch
+    // that dW needs (22 tokens of 232 <- 1584: 11.7 us apart, 13.8 together; 6 of
+    // 192 <- 248: 9.2 and 7.7)
+    if constexpr (!glu) {
+      const bool large = kEpi == moe::kEpiDGlu || (long)p.K * p.k_segs * p.N >= kSmallWeights;
+      if (p.b_mn && !p.a_mn && large && few_tokens(p.M, p.K * p.k_segs)) {
+        TRY((rows<kEpi, true>(dv, one, false, st, what)));
+        continue;
+      }
+    }
+    const SplitChoice c = pick_split(dv, one, glu, kEpi == moe::kEpiLinear && p.b_mn, kPieces ? kPieceStages : 1 << 30);
     if (c.splits) TRY(split<kEpi>(dv, one, c, st, what));
     else rest.take(one);
   }
@@ -487,32 +532,6 @@ moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* wha
                dim3((unsigned)ctas), moe::dense_gemm_threads(), moe::dense_gemm_smem_bytes(), pt.cg, st, part.g));
   }
   return MOE_OK;
-}
-
-// Few tokens: the weights' rows over clusters that split K, down to two stages
-// of 64 k a CTA while there are fewer CTAs than SMs, four beyond (24 x 1024 ->
-// 1024: 3.9 us with 8 splits, 4.3 with 4; 24 x 1024 -> 4096: 6.4 with 8, 4.9
-// with 4). Above 32 tokens a K below 512 leaves nothing to split, and the tiled
-// kernel is faster (64 x 256 -> 256: 4.2 us and 5.9).
-bool few_tokens(int T, int K) { return T <= moe::kRowsTokens && (T <= 32 || K >= 512); }
-template <int kEpi>
-moe_status rows(const Device& dv, const Launch& l, bool early, cudaStream_t st, const char* what) {
-  constexpr bool glu = kEpi == moe::kEpiGlu;
-  moe::DenseRowsArgs r;
-  r.g = l.g;
-  r.early = early;
-  moe::DenseProblem& p = r.g.p[0];
-  r.g.tile_n = (p.M + 15) / 16 * 16;
-  const Mat &x = l.a[0][0], *w = l.b[0];
-  TRY(map16(&p.map_b[0], x.p, r.g.f16, x.rows, x.cols, x.ld, r.g.tile_n, what));
-  for (int i = 0; i < (glu ? 2 : 1); ++i)
-    TRY(map16(&p.map_a[i], w[i].p, r.g.f16, w[i].rows, w[i].cols, w[i].ld, glu ? 64 : 128, what));
-  const int tile = glu ? 64 : 128, tiles = (p.N + tile - 1) / tile, ks = (p.K + 63) / 64;
-  r.splits = std::max(std::min(dv.num_sms / tiles, ks / 2), std::min(7 * dv.num_sms / 4 / tiles, ks / 4));
-  r.splits = std::max(1, std::min(moe::kRowsSplits, r.splits));
-  r.stages = moe::dense_rows_stages(p.M, r.g.tile_n);
-  return launch(what, moe::k_dense_rows<kEpi>, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads,
-                moe::dense_rows_smem_bytes(), r.splits, st, r);
 }
 
 // y[T, N] = f(x W^T + bias) + residual

@@ -1,5 +1,7 @@
 // Projections of few tokens (serving steps): y = f(x W^T + b) + r and the gated
-// block's h, bound by the stream of the weights.
+// block's h, bound by the stream of the weights; and of few tokens' gradients
+// dX = dZ W and the block's hidden gradient (kWMn: the weights' output
+// dimension is the contiguous one).
 //
 // A tile is 128 weight rows (the gated block: 64 gate and the same 64 up
 // rows) and all tokens, on tcgen05 with the weights as the M side. The CTAs of
@@ -103,6 +105,26 @@ MOE_DEV void add4(int f16, uint2 w, float (&v)[4]) {
   for (int i = 0; i < 4; ++i) v[i] += t[i];
 }
 
+// g or u as the forward pass saved them: 4 columns, or one
+MOE_DEV void saved4(const DenseGemmArgs& a, const void* q, const uint8_t* s, int row, int c, float (&v)[4]) {
+  const size_t o = (size_t)row * a.p[0].N + c;
+  if (a.saved8) {
+    e4m3_unquad(*reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(q) + o),
+                e8m0_to_f32(s[(size_t)row * ((a.p[0].N + 31) / 32) + c / 32]), v);
+  } else {
+    const uint2 w = load4(q, o);
+    unpack16(a.f16, w.x, v[0], v[1]);
+    unpack16(a.f16, w.y, v[2], v[3]);
+  }
+}
+MOE_DEV float saved1(const DenseGemmArgs& a, const void* q, const uint8_t* s, int row, int c) {
+  const size_t o = (size_t)row * a.p[0].N + c;
+  if (!a.saved8) return load16(a.f16, q, o);
+  float v[4];
+  e4m3_unquad(static_cast<const uint8_t*>(q)[o], e8m0_to_f32(s[(size_t)row * ((a.p[0].N + 31) / 32) + c / 32]), v);
+  return v[0];
+}
+
 // Kept sums: groups of 4 outputs, token by token, this CTA's share of the
 // cluster's in whole warps, so eight lanes hold a 32-column block.
 template <int kEpi>
@@ -115,7 +137,26 @@ MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int 
     const uint32_t off = on ? (uint32_t)((t * 128 + m) * 4) : 0u;
     const size_t o = (size_t)t * a.p[0].N + c;
     float v[4];
-    if (kEpi == kEpiGlu) {
+    if (kEpi == kEpiDGlu) {
+      float g[4], u[4], f[4], d[4];
+      if (on) {
+        saved4(a, a.g, a.g_s, t, c, g);
+        saved4(a, a.u, a.u_s, t, c, u);
+      }
+      sum_kept(part, off, S, v);
+      if (on) {
+        fn_slopes(a.fn, g, f, d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          d[k] *= v[k] * u[k];          // dg
+          v[k] *= f[k];                 // du
+          u[k] *= f[k];                 // h
+        }
+        store4(a.p[0].out[0], o, a.f16, d);
+        store4(a.p[0].out[1], o, a.f16, v);
+        store4(a.pre, o, a.f16, u);
+      }
+    } else if (kEpi == kEpiGlu) {
       float u[4];
       sum_kept(part, off, S, v);
       sum_kept(part, off + 256, S, u);          // the up rows, 64 further on
@@ -153,7 +194,7 @@ MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int 
 
 }  // namespace
 
-template <int kEpi>
+template <int kEpi, bool kWMn>
 __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_constant__ DenseRowsArgs p) {
   const DenseGemmArgs& a = p.g;
   const DenseProblem& b = a.p[0];
@@ -172,7 +213,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   const int stage_bytes = dense_rows_stage(tn);
   const int S = p.splits, rank = (int)blockIdx.x % S;
   const int n0 = (int)blockIdx.x / S * kRows;
-  const int ks = (b.K + 63) / 64;
+  const int ks1 = (b.K + 63) / 64, ks = ks1 * b.k_segs;
   const int j0 = (int)((long)ks * rank / S), j1 = (int)((long)ks * (rank + 1) / S);
   const uint32_t tcols = tn <= 32 ? 32u : 64u;
   // pushed: units of 4 tokens x 32 rows, [unit slot][rank][kUnit] of 4 tokens of a
@@ -201,16 +242,21 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
     if (tc::elect_one()) {
       auto load_w = [&](int s, int j) {
         uint8_t* st = smem + s * stage_bytes;
+        const int seg = j >= ks1 ? 1 : 0, k0 = 64 * (j - seg * ks1);
         mbar_expect_tx(&full[s], (uint32_t)stage_bytes);
         if (kEpi == kEpiGlu) {
-          tc::tma_load_2d(st, &b.map_a[0], 64 * j, n0, &full[s]);
-          tc::tma_load_2d(st + 8192, &b.map_a[1], 64 * j, n0, &full[s]);
+          tc::tma_load_2d(st, &b.map_a[0], k0, n0, &full[s]);
+          tc::tma_load_2d(st + 8192, &b.map_a[1], k0, n0, &full[s]);
+        } else if (kWMn) {
+          tc::tma_load_2d(st, &b.map_a[seg], n0, k0, &full[s]);
+          tc::tma_load_2d(st + 8192, &b.map_a[seg], n0 + 64, k0, &full[s]);
         } else {
-          tc::tma_load_2d(st, &b.map_a[0], 64 * j, n0, &full[s]);
+          tc::tma_load_2d(st, &b.map_a[0], k0, n0, &full[s]);
         }
       };
       auto load_x = [&](int s, int j) {
-        tc::tma_load_2d(smem + s * stage_bytes + 16384, &b.map_b[0], 64 * j, 0, &full[s]);
+        const int seg = j >= ks1 ? 1 : 0;
+        tc::tma_load_2d(smem + s * stage_bytes + 16384, &b.map_b[seg], 64 * (j - seg * ks1), 0, &full[s]);
       };
       if (!p.early) pdl_wait();
       const int pre = min(nst, j1 - j0);
@@ -236,16 +282,17 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
     // ---------------- MMA issuer ----------------
     pdl_wait();                         // its bounded waits begin when the tokens can arrive
     if (tc::elect_one()) {
-      const uint32_t idesc = tc::idesc_16(a.f16, 128, tn, false, false);
+      const uint32_t idesc = tc::idesc_16(a.f16, 128, tn, kWMn, false);
+      constexpr uint32_t w_step = kWMn ? 2048 >> 4 : 32 >> 4;
       int s = 0;
       uint32_t ph = 0;
       for (int j = j0; j < j1; ++j) {
         if (!tc::wait_bounded(&full[s], ph, abort)) break;
         const uint32_t sa = smem_u32(smem + s * stage_bytes);
-        const uint64_t da = tc::desc_sw128(sa), db = tc::desc_sw128(sa + 16384);
+        const uint64_t da = kWMn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa), db = tc::desc_sw128(sa + 16384);
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb)
-          tc::mma_16<1>(tbase, da + 2u * kb, db + 2u * kb, idesc, (j > j0 || kb > 0) ? 1u : 0u);
+          tc::mma_16<1>(tbase, da + kb * w_step, db + 2u * kb, idesc, (j > j0 || kb > 0) ? 1u : 0u);
         tc::commit_cg<1>(&empty[s]);
         if (++s == nst) { s = 0; ph ^= 1u; }
       }
@@ -316,7 +363,17 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       if (t + k >= b.M) break;                      // the same in every lane
       const bool on = c < b.N;
       const size_t o = (size_t)(t + k) * b.N + c;
-      if (kEpi == kEpiGlu) {
+      if (kEpi == kEpiDGlu) {
+        if (on) {
+          const float g[1] = {saved1(a, a.g, a.g_s, t + k, c)};
+          const float u = saved1(a, a.u, a.u_s, t + k, c);
+          float f[1], d[1];
+          fn_slopes(a.fn, g, f, d);
+          store16(b.out[0], o, a.f16, v[k] * u * d[0]);
+          store16(b.out[1], o, a.f16, v[k] * f[0]);
+          store16(a.pre, o, a.f16, f[0] * u);
+        }
+      } else if (kEpi == kEpiGlu) {
         if (a.g && a.saved8) {
           store_lanes8(a, a.g, a.g_s, t + k, c, v[k], on, lane);
           store_lanes8(a, a.u, a.u_s, t + k, c, up[k], on, lane);
@@ -355,7 +412,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   }
 }
 
-template __global__ void k_dense_rows<kEpiLinear>(const __grid_constant__ DenseRowsArgs);
-template __global__ void k_dense_rows<kEpiGlu>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiLinear, false>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiGlu, false>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiLinear, true>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiDGlu, true>(const __grid_constant__ DenseRowsArgs);
 
 }  // namespace moe

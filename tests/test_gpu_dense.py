@@ -158,6 +158,11 @@ LINEAR_GRAD = [
     (130, 264, 392, HF, "none", True, True),
     (300, 1000, 520, BF, "gelu", True, False),
     (777, 328, 1352, HF, "silu", False, False),
+    # few tokens against large weights; T above the few with long sums
+    (2, 2056, 1000, BF, "silu", True, False),
+    (9, 1000, 776, HF, "none", True, True),
+    (50, 1288, 520, HF, "gelu", True, False),
+    (70, 4104, 264, BF, "relu", True, False),
 ]
 
 
