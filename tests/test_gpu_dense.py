@@ -71,6 +71,10 @@ LINEAR = [
     (129, 520, 5000, HF, "gelu", True, True, True),
     (300, 200, 4104, BF, "none", False, True, False),
     (1000, 512, 2048, BF, "relu", True, True, False),
+    # several tiles a CTA
+    (2100, 5008, 328, HF, "silu", True, True, False),
+    (1500, 3336, 1096, BF, "none", False, True, True),
+    (130, 21000, 72, BF, "none", True, False, False),
 ]
 
 
@@ -100,11 +104,14 @@ def test_linear_on_pitched_rows(T):
     x, w, r = rand((T, K), 1, dt, 1), rand((N, K), 0.05, dt, 2), rand((T, N), 1, dt, 4)
     xv, _ = pitched(x, 256)
     rv, _ = pitched(r, 272)
-    yv, ybuf = pitched(torch.zeros_like(r), 320, 7.0)
+    _, ybuf = pitched(torch.zeros(T + 3, N, dtype=dt), 320, 7.0)
+    ybuf[T:] = 7.0
+    yv = ybuf[:T, :N]
     d = M.MoeLinearDims(T=T, N=N, K=K, ldx=256, ldy=320, ldr=272)
     M.moe_linear(d, xv, w, None, rv, yv, None, workspace(M.moe_linear_workspace_size(d)))
     R.check(yv, R.linear(x, w, None, r, "none", dt, dt)[0], "y", 1, dt)
     assert (ybuf[:, N:] == 7.0).all(), "elements between the rows were written"
+    assert (ybuf[T:] == 7.0).all(), "rows behind the last were written"
 
 
 @pytest.mark.parametrize("T", [1, 20, 300])
@@ -163,6 +170,8 @@ LINEAR_GRAD = [
     (9, 1000, 776, HF, "none", True, True),
     (50, 1288, 520, HF, "gelu", True, False),
     (70, 4104, 264, BF, "relu", True, False),
+    (2000, 2056, 3000, BF, "none", False, False),
+    (4100, 1288, 1352, HF, "gelu", True, False),
 ]
 
 
@@ -223,6 +232,8 @@ FFN = [
     (70, 4096, 264, BF, "silu", True, False),
     (200, 2504, 328, HF, "gelu", False, False),
     (1100, 2248, 1544, BF, "silu", True, False),
+    (1100, 2248, 2600, HF, "gelu", True, False),
+    (2500, 520, 4104, BF, "relu", False, False),
 ]
 
 
