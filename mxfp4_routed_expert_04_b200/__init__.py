@@ -361,6 +361,8 @@ def _tensor(t, name, dtype, shape, ld=0, dev=None):
     pitch ld), on the current device. The library itself sees pointers only."""
     if dev is None:
         dev = _device()
+    if t is None:
+        raise _bad(f"{name} is None")
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
             (t.is_contiguous() if not ld or ld == shape[-1] else _pitched(t, shape, ld)):
         return t.data_ptr()

@@ -176,5 +176,7 @@ def test_binding_checks_tensors():
         M.moe_linear(d, ok["x"], ok["w"], None, None, ok["x"], None, torch.zeros(8, dtype=torch.uint8))
     with pytest.raises(M.MoeError, match="2-D"):
         M.moe_ckpt8_pack(torch.zeros(4, 64), None, None)
+    with pytest.raises(M.MoeError, match="x is None"):
+        ptr(None)
     with pytest.raises(M.MoeError, match="SAVE_NONE"):
         M.FfnSaved(blk(), device="cpu")
