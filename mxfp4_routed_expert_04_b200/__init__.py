@@ -356,16 +356,22 @@ def _bad(message):
     return MoeError(1, message)
 
 
-def _tensor(t, name, dtype, shape, ld=0, dev=None):
+def _device():
+    """The current CUDA device (-2, which no tensor is on, without one)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except (RuntimeError, AttributeError):
+        return -2
+
+
+def _tensor(t, name, dtype, shape, ld, dev):
     """Pointer of a tensor after its checks: type, shape, rows packed (or of
-    pitch ld), on the current device. The library itself sees pointers only."""
-    if dev is None:
-        dev = _device()
-    if t is None:
-        raise _bad(f"{name} is None")
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
+    pitch ld), on device dev. The library itself sees pointers only."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.get_device() == dev and \
             (t.is_contiguous() if not ld or ld == shape[-1] else _pitched(t, shape, ld)):
         return t.data_ptr()
+    if t is None:
+        raise _bad(f"{name} is None")
     if t.dtype is not dtype:
         raise _bad(f"{name} is {t.dtype}, not {dtype}")
     if t.shape != shape:
@@ -379,17 +385,12 @@ def _pitched(t, shape, ld):
     return (shape[1] == 1 or t.stride(1) == 1) and (shape[0] == 1 or t.stride(0) == ld)
 
 
-def _device():
-    """The current CUDA device (-2, which no tensor is on, without one)."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
-
-
-def _opt(t, name, dtype, shape, ld=0, dev=None):
+def _opt(t, name, dtype, shape, ld, dev):
     return None if t is None else _tensor(t, name, dtype, shape, ld, dev)
 
 
-def _ws_args(ws, dev=None):
-    if ws.get_device() != (_device() if dev is None else dev) or not ws.is_contiguous():
+def _ws_args(ws, dev):
+    if ws.get_device() != dev or not ws.is_contiguous():
         raise _bad("the workspace is not a contiguous tensor on the current CUDA device")
     return ws.data_ptr(), ws.nbytes
 
@@ -401,13 +402,14 @@ def _raw_stream(stream, dev):
 
 def _types(dims):
     """(16-bit type, output type) of dims; dims out of range are left to the library."""
-    t16 = _TORCH16[1 if dims.dtype == DTYPE_F16 else 0]
+    t16 = _TORCH16[dims.dtype == DTYPE_F16]
     return t16, torch.float32 if dims.out_f32 else t16
 
 
 def moe_dense_workspace_init(ws, stream=None):
-    p, n = _ws_args(ws)
-    _check(_lib.moe_dense_workspace_init(p, n, _stream(stream)))
+    dev = _device()
+    p, n = _ws_args(ws, dev)
+    _check(_lib.moe_dense_workspace_init(p, n, _raw_stream(stream, dev)))
 
 
 def _size(fn, dims):
@@ -514,11 +516,12 @@ def moe_ffn_backward(dims, dy, x, wg, wu, wd, saved, dx, dwg, dwu, dwd, ws, stre
 
 
 def _rows16(t, name, dev):
-    if t.dim() != 2 or t.dtype not in _TORCH16:
+    dtype = t.dtype
+    if t.dim() != 2 or dtype not in _TORCH16:
         raise _bad(f"{name} is not a 2-D bf16 or f16 tensor")
-    rows, cols = t.shape
+    rows, cols = shape = t.shape
     ld = t.stride(0) if rows > 1 else cols
-    return _TORCH16.index(t.dtype), rows, cols, ld, _tensor(t, name, t.dtype, (rows, cols), ld, dev)
+    return int(dtype is torch.float16), rows, cols, ld, _tensor(t, name, dtype, shape, ld, dev)
 
 
 def moe_ckpt8_pack(src, q, s, stream=None):

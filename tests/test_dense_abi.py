@@ -159,7 +159,7 @@ def test_binding_checks_tensors():
     ok = dict(x=torch.zeros(4, 128, dtype=torch.bfloat16), w=torch.zeros(64, 128, dtype=torch.bfloat16))
 
     def ptr(t, ld=0, shape=(4, 128)):
-        return M._tensor(t, "x", torch.bfloat16, shape, ld)
+        return M._tensor(t, "x", torch.bfloat16, shape, ld, M._device())
 
     with pytest.raises(M.MoeError, match="float32"):
         ptr(ok["x"].float())
