@@ -56,6 +56,20 @@ struct DenseGemmArgs {
   int32_t* status;
 };
 
+// Longest sum, in stages of 64 k, in front of an 8-bit checkpoint (K = 1024). A
+// tensor-core sum is cut off towards zero at every step of 16 k and loses about
+// 1.5e-8 of itself each time (random signs; measured 7.8e-6 at K = 8192, fp32
+// FMAs 0). In 16-bit outputs that is nothing, but an 8-bit checkpoint moves a
+// value that lies so close to a border of its grid by a whole step: 3.3e-4 of
+// the codes in one piece of K = 8192, 8e-5 in pieces of 2048. (Sums of one sign
+// lose more: at K = 65536 one code in 100 in one piece, in pieces none beyond
+// the error of 64 steps.) kPieces: the stages of a tile, or of a CTA's part of
+// one, go in pieces of at most this many, each with an accumulator of its own,
+// added up in registers (32 tokens through a block of 8192 / 8192: 76.0 us in
+// pieces, 75.8 in one; 64 through 8192 / 18432: 156.8 and 156.2).
+constexpr int kPieceStages = 16;
+constexpr int pieces_of(int stages) { return (stages + kPieceStages - 1) / kPieceStages; }
+
 template <int kEpi, int kCg, bool kPieces>
 __global__ void k_dense_gemm(const __grid_constant__ DenseGemmArgs a);
 // small products: one tile of 128 rows and 64 or 128 columns per cluster of `splits` CTAs
@@ -92,7 +106,7 @@ constexpr int dense_rows_stages(int T, int tile_n) {
 static_assert(512 * kRowsTokens <= dense_rows_stage(16) * 2, "kept sums fit the ring's first two stages");
 constexpr int kDenseRowsStages = dense_rows_stages(16, 16);
 constexpr size_t dense_rows_smem_bytes() { return kRowsMemory + 1024; }
-template <int kEpi, bool kWMn>
+template <int kEpi, bool kWMn, bool kPieces>
 __global__ void k_dense_rows(const __grid_constant__ DenseRowsArgs a);
 
 // --- element kernels (dense_elem.cu) ------------------------------------------

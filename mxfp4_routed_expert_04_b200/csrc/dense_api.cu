@@ -46,7 +46,6 @@ char* at(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
 
 constexpr size_t kStatusBytes = 256;
 constexpr long kSmallWeights = 1 << 18;
-constexpr int kPieceStages = 16;    // longest sum in front of an 8-bit checkpoint (K = 1024)
 
 moe_status check_width(const char* name, int v) {
   if (v < 8 || v > 65536 || v % 8 != 0)
@@ -177,9 +176,9 @@ cudaError_t allow_smem() {
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int kEpi, bool kWMn>
+template <int kEpi, bool kWMn, bool kPieces = false>
 cudaError_t allow_rows() {
-  return cudaFuncSetAttribute(moe::k_dense_rows<kEpi, kWMn>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(moe::k_dense_rows<kEpi, kWMn, kPieces>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)moe::dense_rows_smem_bytes());
 }
 template <typename K>
@@ -219,6 +218,7 @@ moe_status device(const Device** out) {
     if (e == cudaSuccess) e = allow_smem<moe::kEpiDGlu>();
     if (e == cudaSuccess) e = allow_rows<moe::kEpiLinear, false>();
     if (e == cudaSuccess) e = allow_rows<moe::kEpiGlu, false>();
+    if (e == cudaSuccess) e = allow_rows<moe::kEpiGlu, false, true>();
     if (e == cudaSuccess) e = allow_rows<moe::kEpiLinear, true>();
     if (e == cudaSuccess) e = allow_rows<moe::kEpiDGlu, true>();
     if (e == cudaSuccess)
@@ -483,8 +483,12 @@ moe_status rows(const Device& dv, const Launch& l, bool early, cudaStream_t st, 
   r.splits = std::max(std::min(dv.num_sms / tiles, ks / 2), std::min(7 * dv.num_sms / 4 / tiles, ks / 4));
   r.splits = std::max(1, std::min(moe::kRowsSplits, r.splits));
   r.stages = moe::dense_rows_stages(p.M, r.g.tile_n);
-  return launch(what, moe::k_dense_rows<kEpi, kWMn>, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads,
-                moe::dense_rows_smem_bytes(), r.splits, st, r);
+  auto kernel = moe::k_dense_rows<kEpi, kWMn, false>;
+  if constexpr (glu) {
+    if (r.g.saved8 && (ks + r.splits - 1) / r.splits > moe::kPieceStages) kernel = moe::k_dense_rows<kEpi, kWMn, true>;
+  }
+  return launch(what, kernel, dim3((unsigned)(tiles * r.splits)), moe::kRowsThreads, moe::dense_rows_smem_bytes(),
+                r.splits, st, r);
 }
 
 template <int kEpi, bool kPieces = false>
@@ -507,7 +511,7 @@ moe_status enqueue(const Device& dv, Launch& l, cudaStream_t st, const char* wha
         continue;
       }
     }
-    const SplitChoice c = pick_split(dv, one, glu, kEpi == moe::kEpiLinear && p.b_mn, kPieces ? kPieceStages : 1 << 30);
+    const SplitChoice c = pick_split(dv, one, glu, kEpi == moe::kEpiLinear && p.b_mn, kPieces ? moe::kPieceStages : 1 << 30);
     if (c.splits) TRY(split<kEpi>(dv, one, c, st, what));
     else rest.take(one);
   }

@@ -38,14 +38,6 @@ constexpr int kGroupM = 8;                         // row tiles that share their
 struct Tile {
   int prob, seg, m0, n0;
 };
-// kPieces: pieces of a tile's stages, at most 16 (K = 1024) each, that get
-// accumulators of their own and are added up in registers. A tensor-core sum
-// is cut off towards zero at every step of 16 k and loses about 1.5e-8 of
-// itself each time (random signs; measured 7.8e-6 at K = 8192, fp32 FMAs 0). In
-// 16-bit outputs that is nothing, but an 8-bit checkpoint moves a value that
-// lies so close to a border of its grid by a whole step: 3.3e-4 of the codes in
-// one piece of K = 8192, 8e-5 in pieces of 2048.
-MOE_DEV int pieces_of(int stages) { return (stages + 15) / 16; }
 // f(a_mn, b_mn) as compile-time constants: the directions that the launches use
 template <int kEpi, typename F>
 MOE_DEV void by_direction(const DenseProblem& p, F&& f) {

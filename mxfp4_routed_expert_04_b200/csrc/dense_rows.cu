@@ -194,14 +194,14 @@ MOE_DEV void finish_kept(const DenseGemmArgs& a, const float* part, int n0, int 
 
 }  // namespace
 
-template <int kEpi, bool kWMn>
+template <int kEpi, bool kWMn, bool kPieces>
 __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_constant__ DenseRowsArgs p) {
   const DenseGemmArgs& a = p.g;
   const DenseProblem& b = a.p[0];
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t full[kDenseRowsStages], empty[kDenseRowsStages], acc_full;
+  __shared__ uint64_t full[kDenseRowsStages], empty[kDenseRowsStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   volatile int* abort = &abort_flag;
@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   const int n0 = (int)blockIdx.x / S * kRows;
   const int ks1 = (b.K + 63) / 64, ks = ks1 * b.k_segs;
   const int j0 = (int)((long)ks * rank / S), j1 = (int)((long)ks * (rank + 1) / S);
-  const uint32_t tcols = tn <= 32 ? 32u : 64u;
+  const uint32_t acols = tn <= 32 ? 32u : 64u;              // columns of an accumulator
+  const uint32_t tcols = kPieces ? 2u * acols : acols;
+  const int pieces = kPieces ? pieces_of(j1 - j0) : 1;
   // pushed: units of 4 tokens x 32 rows, [unit slot][rank][kUnit] of 4 tokens of a
   // row, behind the ring; kept: floats [token][128 rows], over it
   const bool push = b.M <= kRowsPush;
@@ -226,7 +228,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
-    mbar_init(&acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -236,6 +241,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   cluster_arrive();                     // this CTA runs: its memory may be written
   tc::fence_after_sync();
   const uint32_t tbase = tmem_slot;
+  const int wq = warp & 3;              // warps 2-5: which 32 of the 128 rows
+  const uint32_t row0 = tbase + ((uint32_t)(32 * wq) << 16);
+  float sum[kPieces ? kRowsTokens : 1]; // kPieces: this lane's row, all tokens
+  bool whole = true;
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -286,49 +295,99 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       constexpr uint32_t w_step = kWMn ? 2048 >> 4 : 32 >> 4;
       int s = 0;
       uint32_t ph = 0;
-      for (int j = j0; j < j1; ++j) {
-        if (!tc::wait_bounded(&full[s], ph, abort)) break;
-        const uint32_t sa = smem_u32(smem + s * stage_bytes);
-        const uint64_t da = kWMn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa), db = tc::desc_sw128(sa + 16384);
+      bool ok = true;
+      for (int i = 0; i < pieces && ok; ++i) {
+        const int buf = i & 1;
+        const int b0 = kPieces ? j0 + (j1 - j0) * i / pieces : j0, b1 = kPieces ? j0 + (j1 - j0) * (i + 1) / pieces : j1;
+        if (kPieces) {
+          ok = tc::wait_bounded(&acc_empty[buf], (uint32_t)((i >> 1) & 1) ^ 1u, abort);
+          tc::fence_after_sync();
+        }
+        const uint32_t d = tbase + acols * (uint32_t)buf;
+        for (int j = b0; j < b1 && ok; ++j) {
+          if (!tc::wait_bounded(&full[s], ph, abort)) { ok = false; break; }
+          const uint32_t sa = smem_u32(smem + s * stage_bytes);
+          const uint64_t da = kWMn ? tc::desc_mn_sw128(sa, 8192) : tc::desc_sw128(sa), db = tc::desc_sw128(sa + 16384);
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
-          tc::mma_16<1>(tbase, da + kb * w_step, db + 2u * kb, idesc, (j > j0 || kb > 0) ? 1u : 0u);
-        tc::commit_cg<1>(&empty[s]);
-        if (++s == nst) { s = 0; ph ^= 1u; }
+          for (int kb = 0; kb < 4; ++kb)
+            tc::mma_16<1>(d, da + kb * w_step, db + 2u * kb, idesc, (j > b0 || kb > 0) ? 1u : 0u);
+          tc::commit_cg<1>(&empty[s]);
+          if (++s == nst) { s = 0; ph ^= 1u; }
+        }
+        tc::commit_cg<1>(&acc_full[buf]);       // also when it gave up: no MMA may run past the CTA's exit
       }
-      tc::commit_cg<1>(&acc_full);      // also when it gave up: no MMA may run past the CTA's exit
     }
     __syncwarp();
   } else {
-    // ---------------- partial sums to shared memory (warps 2-5) ----------------
+    // ---------------- sums (warps 2-5; to shared memory further down) ----------------
     pdl_wait();
+    if constexpr (kPieces) {
+      // The pieces as they come, in order. In front of the cluster barrier: the
+      // MMAs wait for these warps, and warps 0 and 1 come to it behind the MMAs.
+      pdl_trigger();
+      for (int i = 0; i < pieces && whole; ++i) {
+        whole = __all_sync(0xFFFFFFFFu, tc::wait_bounded(&acc_full[i & 1], (uint32_t)((i >> 1) & 1), abort));
+        if (!whole) break;
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < kRowsTokens / 16; ++c) {
+          if (16 * c < b.M) {
+            uint32_t d[32];
+            tc::ld_16cols(row0 + acols * (uint32_t)(i & 1) + 16 * c, d);
+            tc::wait_ld();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum[16 * c + k] = __uint_as_float(d[k]) + (i ? sum[16 * c + k] : 0.0f);
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&acc_empty[i & 1]);
+      }
+    }
   }
   pdl_trigger();
   cluster_wait();
   if (warp >= 2) {
-    const int wq = warp & 3;            // which 32 of the 128 rows
-    const bool ok = tc::wait_bounded(&acc_full, 0, abort);
-    if (__all_sync(0xFFFFFFFFu, ok)) {  // the sums are complete
-      tc::fence_after_sync();
-      const uint32_t at = (uint32_t)(rank * kUnit + (kEpi == kEpiGlu ? 32 * (wq >> 1) : 0) + lane) * 16u;
-      int slot = 0, owner = wq & (kPer - 1);        // of unit kPer * (token / 4) + this warp's rows
-      for (int c0 = 0; c0 < b.M; c0 += 16) {
-        uint32_t d[32];
-        tc::ld_16cols(tbase + ((uint32_t)(32 * wq) << 16) + c0, d);
-        tc::wait_ld();
+    const uint32_t at = (uint32_t)(rank * kUnit + (kEpi == kEpiGlu ? 32 * (wq >> 1) : 0) + lane) * 16u;
+    int slot = 0, owner = wq & (kPer - 1);          // of unit kPer * (token / 4) + this warp's rows
+    // this lane's row and tokens c0.. of the finished sums, to where they are added up
+    auto give = [&](int c0, const uint32_t* d) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          if (c0 + i < b.M) {
-            if (push) {
-              while (owner >= S) { owner -= S; ++slot; }
-              st_cluster4(tc::mapa(parts, (uint32_t)owner) + (uint32_t)(slot * S * kUnit * 16) + at, d + i);
-              owner += kPer;
-            } else {
+      for (int i = 0; i < 16; i += 4) {
+        if (c0 + i < b.M) {
+          if (push) {
+            while (owner >= S) { owner -= S; ++slot; }
+            st_cluster4(tc::mapa(parts, (uint32_t)owner) + (uint32_t)(slot * S * kUnit * 16) + at, d + i);
+            owner += kPer;
+          } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                sts32(smem_u32(parts) + (uint32_t)(((c0 + i + k) * 128 + 32 * wq + lane) * 4), d[i + k]);
-            }
+            for (int k = 0; k < 4; ++k)
+              sts32(smem_u32(parts) + (uint32_t)(((c0 + i + k) * 128 + 32 * wq + lane) * 4), d[i + k]);
           }
+        }
+      }
+    };
+    if constexpr (kPieces) {
+      if (whole) {
+#pragma unroll
+        for (int c = 0; c < kRowsTokens / 16; ++c) {
+          if (16 * c < b.M) {
+            uint32_t d[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) d[k] = __float_as_uint(sum[16 * c + k]);
+            give(16 * c, d);
+          }
+        }
+      }
+    } else {
+      const bool ok = tc::wait_bounded(&acc_full[0], 0, abort);
+      if (__all_sync(0xFFFFFFFFu, ok)) {  // the sums are complete
+        tc::fence_after_sync();
+        for (int c0 = 0; c0 < b.M; c0 += 16) {
+          uint32_t d[32];
+          tc::ld_16cols(row0 + c0, d);
+          tc::wait_ld();
+          give(c0, d);
         }
       }
     }
@@ -412,9 +471,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   }
 }
 
-template __global__ void k_dense_rows<kEpiLinear, false>(const __grid_constant__ DenseRowsArgs);
-template __global__ void k_dense_rows<kEpiGlu, false>(const __grid_constant__ DenseRowsArgs);
-template __global__ void k_dense_rows<kEpiLinear, true>(const __grid_constant__ DenseRowsArgs);
-template __global__ void k_dense_rows<kEpiDGlu, true>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiLinear, false, false>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiGlu, false, false>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiGlu, false, true>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiLinear, true, false>(const __grid_constant__ DenseRowsArgs);
+template __global__ void k_dense_rows<kEpiDGlu, true, false>(const __grid_constant__ DenseRowsArgs);
 
 }  // namespace moe

@@ -208,3 +208,31 @@ def unpack8(q, s):
     sc = torch.exp2(s.double() - 127)
     sc = torch.where(s == 255, torch.full_like(sc, math.nan), sc)
     return t[q.long()] * sc.repeat_interleave(32, dim=1)[:, :q.shape[1]]
+
+
+def scale8(a):
+    """Scale codes of blocks whose largest magnitudes are a (fp64)."""
+    m, e = torch.frexp(a / 448)
+    return (torch.where(m == 0.5, e - 1, e) + 127).clamp(0, 254)
+
+
+def codes8(v, s):
+    """Magnitude codes of v [rows, cols] under the scale codes s, nearest (ties are not looked after)."""
+    mags = torch.tensor(e4m3_table()[:127], dtype=torch.float64, device=v.device)
+    sc = torch.exp2(127 - s.double()).repeat_interleave(32, dim=1)[:, :v.shape[1]]
+    return torch.bucketize(v * sc, (mags[1:] + mags[:-1]) / 2)
+
+
+def check_codes(v, rel, q, s, name):
+    """Codes q and scales s of values known to be within rel of v (fp64, all
+    positive): wherever no border of the grid lies that close, the code is v's.
+    Returns how many elements that holds for."""
+    top = torch.nn.functional.pad(v, (0, -v.shape[1] % 32)).reshape(v.shape[0], -1, 32).amax(-1)
+    lo, hi = scale8(top * (1 - rel)), scale8(top * (1 + rel))
+    sure = lo == hi
+    assert torch.equal(s[sure].long(), lo[sure]), f"{name}: scales"
+    lo, hi = codes8(v * (1 - rel), s), codes8(v * (1 + rel), s)
+    sure = (lo == hi) & sure.repeat_interleave(32, dim=1)[:, :v.shape[1]]
+    off = int((q.long() != lo)[sure].sum())
+    assert off == 0, f"{name}: {off} of {int(sure.sum())} codes are off"
+    return int(sure.sum())

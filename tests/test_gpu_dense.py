@@ -588,3 +588,40 @@ def test_a_training_step_of_a_stack(save):
             ("dx", "dwi", "dbi", "dwg", "dwu", "dwd", "dwo"), (dx, dwi, dbi, dw["wg"], dw["wu"], dw["wd"], dwo), leaves)]:
         rel = ((got.double() - ref).norm() / ref.norm()).item()
         assert rel <= tol, f"{n}: {rel:.3e} above {tol:.3e}"
+
+
+# --- sums in front of a checkpoint --------------------------------------------------------
+
+LONG_H, LONG_I = 65536, 9536
+
+
+@pytest.fixture(scope="module")
+def long_sums():
+    """Positive x and weights of the longest contraction, and the exact g and u."""
+    x = rand((130, LONG_H), 1, BF, 1).abs()
+    w = [rand((LONG_I, LONG_H), 2e-3, BF, 2 + i).abs() for i in range(2)]
+    exact = [torch.cat([x.double() @ c.double().t() for c in m.split(1192)], dim=1) for m in w]
+    yield x, w, exact
+    del x, w, exact
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,I", [(1, LONG_I), (8, LONG_I), (9, LONG_I), (40, LONG_I), (64, LONG_I), (65, LONG_I),
+                                 (130, LONG_I), (8, 4104), (40, 4104), (3, 72), (64, 72), (130, 72)])
+def test_codes_of_long_sums(long_sums, T, I):
+    """The 8-bit g and u of K = 65536. All products are positive, so no partial
+    sum is above the whole, S. In pieces of K = 1024 a tensor-core sum has 64
+    additions, each off by at most 2^-23 of its piece: the pieces together by
+    64 * 2^-23 S; adding up 64 pieces and the parts of up to 8 CTAs rounds 72
+    times by 2^-24 S. In one piece of all K, 4096 additions cut
+    off, one code in 100 is another."""
+    x, w, exact = long_sums
+    d = M.MoeFfnDims(T=T, H=LONG_H, I=I, fn=1, save=M.SAVE_8)
+    saved, y = M.FfnSaved(d, keep_x=False), empty((T, LONG_H), BF)
+    wd = torch.zeros((LONG_H, I), dtype=BF, device="cuda")
+    ws = workspace(M.moe_ffn_workspace_size(d))
+    M.moe_ffn(d, x[:T], w[0][:I], w[1][:I], wd, None, y, saved, ws)
+    rel = 64 * 2.0 ** -23 + 72 * 2.0 ** -24
+    for n, v, q, s in (("g", exact[0], saved.g, saved.g_s), ("u", exact[1], saved.u, saved.u_s)):
+        assert R.check_codes(v[:T, :I], rel, q, s, n) > 0.99 * T * I
+    assert (y == 0).all() and M.moe_device_status(ws) == 0
