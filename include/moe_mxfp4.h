@@ -60,7 +60,7 @@ extern "C" {
 
 typedef enum {
   MOE_OK = 0,
-  MOE_ERR_INVALID_ARG = 1,        /* null pointer, null dims, bad enum */
+  MOE_ERR_INVALID_ARG = 1,        /* null pointer, null dims, bad enum, overlap */
   MOE_ERR_UNSUPPORTED_SHAPE = 2,  /* a dimension outside the supported set */
   MOE_ERR_ALIGNMENT = 3,          /* a pointer not 16-byte aligned */
   MOE_ERR_WORKSPACE_TOO_SMALL = 4,
@@ -418,8 +418,11 @@ moe_status moe_layer(const moe_dims* dims, const moe_layer_args* args,
  *   of 8, not below the row's length and below 2^31. Elements between a row's
  *   end and the next row are neither read nor written. Weights, weight
  *   gradients and saved activations are packed.
- * - y may be the residual itself (the same pointer and pitch, 16-bit output);
- *   otherwise outputs overlap no input and no other output.
+ * - y may be the residual itself (the same pointer and pitch, 16-bit output),
+ *   and in moe_ffn it may lie on x, which is read before y is written.
+ *   Otherwise no output and no workspace may share a byte with what the call
+ *   reads, nor with one another (MOE_ERR_INVALID_ARG): y = x + f(W x) is no
+ *   moe_linear into x. Slices of one buffer, side by side, share none.
  * - Infinities and NaN propagate as IEEE arithmetic has them, within the rows
  *   and columns that use them.
  * - Results are the same bits on every call with the same inputs: no sum

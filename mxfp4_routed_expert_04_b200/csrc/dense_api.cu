@@ -9,6 +9,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <utility>
 
 #include "../../include/moe_mxfp4.h"
 #include "dense.h"
@@ -81,6 +82,74 @@ moe_status launched(cudaError_t e, const char* what) {
   if (e != cudaSuccess) return fail(MOE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
   return MOE_OK;
 }
+
+// --- overlap ------------------------------------------------------------------
+// A buffer as the bytes that a call touches: rows of `width` bytes, `pitch` apart.
+struct Span {
+  const char* name;
+  uintptr_t p;
+  size_t rows, width, pitch;
+};
+// whether they share a byte, exactly (slices of one buffer, side by side, do not)
+bool overlap(Span a, Span b) {
+  if (b.p < a.p) std::swap(a, b);
+  if (b.p >= a.p + (a.rows - 1) * a.pitch + a.width) return false;
+  size_t i = (b.p - a.p) / a.pitch, j = 0;
+  if (a.pitch == b.pitch) {             // b's rows start in the same place of each of a's
+    const size_t d = b.p - a.p - i * a.pitch;
+    return d < a.width || d + b.width > a.pitch;
+  }
+  while (i < a.rows && j < b.rows) {    // both in order of address
+    const uintptr_t x = a.p + i * a.pitch, y = b.p + j * b.pitch;
+    if (x < y + b.width && y < x + a.width) return true;
+    if (x < y) ++i;
+    else ++j;
+  }
+  return false;
+}
+// The buffers of a call. CTAs write their outputs while others still read, so an
+// output may share no byte with what the call reads, nor with another output.
+class Spans {
+ public:
+  void in(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t bytes) {
+    add(in_, n_in_, name, p, rows, cols, ld, bytes);
+  }
+  void out(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t bytes) {
+    add(out_, n_out_, name, p, rows, cols, ld, bytes);
+  }
+  // an input that the first output may lie on
+  void free_in(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, size_t bytes) {
+    add(free_, n_free_, name, p, rows, cols, ld, bytes);
+  }
+  moe_status check() const {
+    for (int o = 0; o < n_out_; ++o) {
+      for (int k = o + 1; k < n_out_; ++k) TRY(pair(out_[o], out_[k]));
+      for (int k = 0; k < n_in_; ++k) TRY(pair(out_[o], in_[k]));
+      for (int k = 0; k < n_free_ && o > 0; ++k) TRY(pair(out_[o], free_[k]));
+    }
+    return MOE_OK;
+  }
+
+ private:
+  static constexpr int kMost = 10;      // the inputs of moe_ffn_backward from 8 bits
+  Span in_[kMost], out_[kMost], free_[2];
+  int n_in_ = 0, n_out_ = 0, n_free_ = 0;
+
+  static void add(Span* to, int& n, const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld,
+                  size_t bytes) {
+    if (!p) return;
+    if (ld == cols || rows == 1) {      // packed: one row
+      cols *= rows;
+      ld = cols;
+      rows = 1;
+    }
+    to[n++] = {name, reinterpret_cast<uintptr_t>(p), (size_t)rows, (size_t)cols * bytes, (size_t)ld * bytes};
+  }
+  static moe_status pair(const Span& a, const Span& b) {
+    if (overlap(a, b)) return fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+    return MOE_OK;
+  }
+};
 
 // --- plans --------------------------------------------------------------------
 
@@ -648,6 +717,16 @@ moe_status moe_linear(const moe_linear_dims* dims, const void* x, const void* w,
   if (y == residual && (p.out_f32 || p.ldy != p.ldr))
     return fail(MOE_ERR_INVALID_ARG, "y is the residual, but not of its type and pitch");
   TRY(check_ws(ws, ws_bytes, p.total));
+  Spans b;
+  b.out("y", y, p.T, p.N, p.ldy, p.out_f32 ? 4 : 2);
+  b.out("pre", pre, p.T, p.N, p.N, 2);
+  b.out("the workspace", ws, 1, (int64_t)p.total, (int64_t)p.total, 1);
+  b.in("x", x, p.T, p.K, p.ldx, 2);
+  b.in("w", w, p.N, p.K, p.K, 2);
+  b.in("bias", bias, 1, p.N, p.N, 2);
+  if (residual == y) b.free_in("residual", residual, p.T, p.N, p.ldr, 2);
+  else b.in("residual", residual, p.T, p.N, p.ldr, 2);
+  TRY(b.check());
   const Device* dv;
   TRY(device(&dv));
   return project(*dv, p.T, p.N, p.K, p.f16, p.fn, p.out_f32, x, p.ldx, w, bias, residual, p.ldr, y, p.ldy, pre, ws,
@@ -669,6 +748,17 @@ moe_status moe_linear_backward(const moe_linear_dims* dims, const void* dy, cons
   MAYBE(dw);
   MAYBE(dbias);
   TRY(check_ws(ws, ws_bytes, p.total));
+  const size_t ob = p.out_f32 ? 4 : 2;
+  Spans b;
+  b.out("dx", dx, p.T, p.K, p.ldx, ob);
+  b.out("dw", dw, p.N, p.K, p.K, ob);
+  b.out("dbias", dbias, 1, p.N, p.N, ob);
+  b.out("the workspace", ws, 1, (int64_t)p.total, (int64_t)p.total, 1);
+  b.in("dy", dy, p.T, p.N, p.ldy, 2);
+  b.in("pre", pre, p.T, p.N, p.N, 2);
+  if (dx) b.in("w", w, p.N, p.K, p.K, 2);
+  if (dw) b.in("x", x, p.T, p.K, p.ldx, 2);
+  TRY(b.check());
   const Device* dv;
   TRY(device(&dv));
   cudaStream_t st = (cudaStream_t)stream;
@@ -714,6 +804,26 @@ moe_status moe_ffn(const moe_ffn_dims* dims, const void* x, const void* wg, cons
     return fail(MOE_ERR_INVALID_ARG, "y is the residual, but not of its type and pitch");
   TRY(check_saved(p, saved));
   TRY(check_ws(ws, ws_bytes, p.total));
+  const int64_t nh = (p.H + 31) / 32, ni = (p.I + 31) / 32;
+  Spans b;
+  b.out("y", y, p.T, p.H, p.ldy, p.out_f32 ? 4 : 2);
+  if (saved) {
+    const size_t sb = p.save == MOE_SAVE_8 ? 1 : 2;
+    b.out("saved->g", saved->g, p.T, p.I, p.I, sb);
+    b.out("saved->u", saved->u, p.T, p.I, p.I, sb);
+    b.out("saved->g_s", saved->g_s, p.T, ni, ni, 1);
+    b.out("saved->u_s", saved->u_s, p.T, ni, ni, 1);
+    b.out("saved->x_q", saved->x_q, p.T, p.H, p.H, 1);
+    b.out("saved->x_s", saved->x_s, p.T, nh, nh, 1);
+  }
+  b.out("the workspace", ws, 1, (int64_t)p.total, (int64_t)p.total, 1);
+  b.free_in("x", x, p.T, p.H, p.ldx, 2);        // the down projection writes y behind the last read of x
+  b.in("wg", wg, p.I, p.H, p.H, 2);
+  b.in("wu", wu, p.I, p.H, p.H, 2);
+  b.in("wd", wd, p.H, p.I, p.I, 2);
+  if (residual == y) b.free_in("residual", residual, p.T, p.H, p.ldr, 2);
+  else b.in("residual", residual, p.T, p.H, p.ldr, 2);
+  TRY(b.check());
   const Device* dv;
   TRY(device(&dv));
   cudaStream_t st = (cudaStream_t)stream;
@@ -761,6 +871,30 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dy, const void
   if (dwg && !x && !saved->x_q)
     return fail(MOE_ERR_INVALID_ARG, "x is NULL and saved holds no x_q: the weight gradients need one");
   TRY(check_ws(ws, ws_bytes, p.total));
+  const int64_t nh = (p.H + 31) / 32, ni = (p.I + 31) / 32;
+  const size_t ob = p.out_f32 ? 4 : 2, sb = p.save == MOE_SAVE_8 ? 1 : 2;
+  Spans b;
+  b.out("dx", dx, p.T, p.H, p.ldx, ob);
+  b.out("dwg", dwg, p.I, p.H, p.H, ob);
+  b.out("dwu", dwu, p.I, p.H, p.H, ob);
+  b.out("dwd", dwd, p.H, p.I, p.I, ob);
+  b.out("the workspace", ws, 1, (int64_t)p.total, (int64_t)p.total, 1);
+  b.in("dy", dy, p.T, p.H, p.ldy, 2);
+  b.in("wd", wd, p.H, p.I, p.I, 2);
+  if (dx) {
+    b.in("wg", wg, p.I, p.H, p.H, 2);
+    b.in("wu", wu, p.I, p.H, p.H, 2);
+  }
+  b.in("saved->g", saved->g, p.T, p.I, p.I, sb);
+  b.in("saved->u", saved->u, p.T, p.I, p.I, sb);
+  b.in("saved->g_s", saved->g_s, p.T, ni, ni, 1);
+  b.in("saved->u_s", saved->u_s, p.T, ni, ni, 1);
+  if (dwg && x) b.in("x", x, p.T, p.H, p.ldx, 2);
+  if (dwg && !x) {
+    b.in("saved->x_q", saved->x_q, p.T, p.H, p.H, 1);
+    b.in("saved->x_s", saved->x_s, p.T, nh, nh, 1);
+  }
+  TRY(b.check());
   const Device* dv;
   TRY(device(&dv));
   cudaStream_t st = (cudaStream_t)stream;
@@ -792,6 +926,11 @@ moe_status moe_ffn_backward(const moe_ffn_dims* dims, const void* dy, const void
 moe_status moe_ckpt8_pack(int32_t dtype, int64_t rows, int32_t cols, const void* src, int64_t ld,
                           uint8_t* q, uint8_t* s, void* stream) {
   TRY(check_ckpt8(dtype, rows, cols, src, &ld, q, s, "src"));
+  Spans b;
+  b.out("q", q, rows, cols, cols, 1);
+  b.out("s", s, rows, (cols + 31) / 32, (cols + 31) / 32, 1);
+  b.in("src", src, rows, cols, ld, 2);
+  TRY(b.check());
   const Device* dv;
   TRY(device(&dv));
   return ckpt8(*dv, true, dtype, rows, cols, src, nullptr, ld, q, s, (cudaStream_t)stream);
@@ -800,6 +939,11 @@ moe_status moe_ckpt8_pack(int32_t dtype, int64_t rows, int32_t cols, const void*
 moe_status moe_ckpt8_unpack(int32_t dtype, int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* s,
                             void* dst, int64_t ld, void* stream) {
   TRY(check_ckpt8(dtype, rows, cols, dst, &ld, q, s, "dst"));
+  Spans b;
+  b.out("dst", dst, rows, cols, ld, 2);
+  b.in("q", q, rows, cols, cols, 1);
+  b.in("s", s, rows, (cols + 31) / 32, (cols + 31) / 32, 1);
+  TRY(b.check());
   const Device* dv;
   TRY(device(&dv));
   return ckpt8(*dv, false, dtype, rows, cols, nullptr, dst, ld, const_cast<uint8_t*>(q), const_cast<uint8_t*>(s),

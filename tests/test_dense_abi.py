@@ -180,3 +180,146 @@ def test_binding_checks_tensors():
         ptr(None)
     with pytest.raises(M.MoeError, match="SAVE_NONE"):
         M.FfnSaved(blk(), device="cpu")
+
+
+# --- outputs that overlap --------------------------------------------------------------
+
+BASE = 1 << 33          # addresses of buffers that nothing reads: a call that is not refused has no GPU to go to
+NO_GPU = pytest.mark.skipif(torch.cuda.is_available(), reason="calls that pass their checks would launch")
+
+
+class Place:
+    """Where every buffer of a call lies: far apart, but for those that `kw` names."""
+
+    def __init__(self, kw):
+        self.kw, self.next = kw, BASE
+
+    def __call__(self, name):
+        self.next += 1 << 26
+        return self.kw.get(name, self.next)
+
+
+def linear_call(dims, res=False, with_pre=False, **kw):
+    p = Place(kw)
+    ws = p("ws")
+    return M._lib.moe_linear(ctypes.byref(dims), p("x"), p("w"), p("bias"), p("residual") if res else None, p("y"),
+                             p("pre") if with_pre else None, ws, BIG, None)
+
+
+def linear_backward_call(dims, want=("dx", "dw", "dbias"), **kw):
+    p = Place(kw)
+    return M._lib.moe_linear_backward(
+        ctypes.byref(dims), p("dy"), p("x"), p("w"), p("pre") if dims.fn else None,
+        *[p(n) if n in want else None for n in ("dx", "dw", "dbias")], p("ws"), BIG, None)
+
+
+def ffn_saved_at(dims, p):
+    n = {0: (), 1: ("g", "u"), 2: ("g", "u", "g_s", "u_s", "x_q", "x_s")}[dims.save]
+    return ctypes.byref(saved(**{k: p(k) for k in n})) if n else None
+
+
+def ffn_call(dims, res=True, **kw):
+    p = Place(kw)
+    s = ffn_saved_at(dims, p)
+    return M._lib.moe_ffn(ctypes.byref(dims), p("x"), p("wg"), p("wu"), p("wd"), p("residual") if res else None, p("y"),
+                          s, p("ws"), BIG, None)
+
+
+def ffn_backward_call(dims, want=("dx", "dwg", "dwu", "dwd"), with_x=True, **kw):
+    p = Place(kw)
+    s = ffn_saved_at(dims, p)
+    return M._lib.moe_ffn_backward(ctypes.byref(dims), p("dy"), p("x") if with_x else None, p("wg"), p("wu"), p("wd"), s,
+                                   *[p(n) if n in want else None for n in ("dx", "dwg", "dwu", "dwd")], p("ws"), BIG,
+                                   None)
+
+
+@pytest.mark.parametrize("call,dims,pairs", [
+    (linear_call, lin(N=128), ["x y", "w y", "bias y", "ws y", "x ws", "w ws"]),
+    (lambda d, **kw: linear_call(d, res=True, with_pre=True, **kw), lin(N=128, fn=1),
+     ["x y", "x pre", "y pre", "residual pre", "w pre", "pre ws", "residual ws"]),
+    (linear_backward_call, lin(fn=1), ["dy dx", "dy dw", "x dx", "x dw", "w dx", "w dw", "pre dx", "pre dw", "dy dbias",
+                                       "pre dbias", "dx dw", "dx dbias", "dw dbias", "dx ws", "dy ws", "pre ws"]),
+    (ffn_call, blk(T=64, save=2), ["wg y", "wu y", "wd y", "x g", "x x_q", "x x_s", "x ws", "wd g_s", "g u", "g g_s",
+                                   "g_s u_s", "g y", "x_q x_s", "residual u", "residual x_q", "ws y", "ws g", "u x_q"]),
+    (ffn_backward_call, blk(save=1), ["dy dx", "dy dwd", "x dx", "x dwg", "wg dx", "wu dwu", "wd dwd", "g dx", "u dwu",
+                                      "dx dwg", "dwg dwu", "dwd dx", "ws dx", "ws g", "ws dy"]),
+    (lambda d, **kw: ffn_backward_call(d, with_x=False, **kw), blk(T=64, save=2),
+     ["x_q dwg", "x_s dx", "g_s dwd", "u_s dx", "ws x_q"]),
+])
+def test_overlapping_buffers_are_refused(call, dims, pairs):
+    """One buffer in two places, and one that begins inside the other."""
+    for pair in pairs:
+        a, b = pair.split()
+        for off in (0, 16):
+            assert call(dims, **{a: BASE, b: BASE + off}) == 1 and "overlaps" in error(), (pair, off)
+            assert call(dims, **{a: BASE + off, b: BASE}) == 1 and "overlaps" in error(), (pair, off)
+
+
+def test_in_place_calls_that_are_refused():
+    """y = x + f(W x) in place: y is the residual, but also the x that other CTAs still read."""
+    assert linear_call(lin(N=128), res=True, x=BASE, residual=BASE, y=BASE) == 1 and "y overlaps x" in error()
+    assert linear_call(lin(N=128, ldx=256, ldy=256), x=BASE, y=BASE + 16) == 1
+    # a residual shifted against y by a row
+    assert linear_call(lin(), res=True, residual=BASE, y=BASE + 128) == 1 and "residual" in error()
+    p = M._lib.moe_ckpt8_pack, M._lib.moe_ckpt8_unpack
+    far = BASE + (1 << 20)
+    assert p[0](0, 4, 64, BASE, 0, BASE, far, None) == 1 and p[0](0, 4, 64, BASE, 0, far, BASE + 496, None) == 1
+    assert p[0](0, 4, 64, far, 0, BASE, BASE + 240, None) == 1 and "overlaps" in error()
+    assert p[1](0, 4, 64, BASE, far, BASE + 240, 0, None) == 1 and p[1](0, 4, 64, far, BASE, BASE, 0, None) == 1
+
+
+@NO_GPU
+def test_neighbours_are_not_refused():
+    """Buffers side by side, or woven into each other's gaps, and what a call does not read."""
+    def passes(status):
+        return status == 5 or pytest.fail(f"status {status}: {error()}")      # no device: behind all the checks
+
+    # [x | y] and [y | x], column slices of one buffer; x between y's rows with another pitch
+    d = lin(N=64, K=64, ldx=128, ldy=128)
+    passes(linear_call(d, x=BASE, y=BASE + 128))
+    passes(linear_call(d, x=BASE + 128, y=BASE))
+    assert linear_call(d, x=BASE, y=BASE + 112) == 1
+    assert linear_call(d, x=BASE, y=BASE + 144) == 1
+    passes(linear_call(lin(T=2, N=64, K=64, ldx=64, ldy=256), x=BASE + 128, y=BASE))        # 2 rows in a gap
+    assert linear_call(lin(T=4, N=64, K=64, ldx=64, ldy=256), x=BASE + 128, y=BASE) == 1    # 4 rows do not fit
+    # back to back
+    passes(linear_call(lin(), y=BASE, x=BASE + 4 * 64 * 2))
+    passes(linear_call(lin(), x=BASE, y=BASE + 4 * 128 * 2))
+    # y into its residual; the block's y into x, with x as the residual or not
+    passes(linear_call(lin(), res=True, residual=BASE, y=BASE))
+    for save in (0, 1, 2):
+        passes(ffn_call(blk(save=save), res=False, x=BASE, y=BASE))
+        passes(ffn_call(blk(save=save), x=BASE, residual=BASE, y=BASE))
+    # gradients over what the call does not read
+    passes(linear_backward_call(lin(), want=("dx",), x=BASE, dx=BASE))
+    passes(linear_backward_call(lin(), want=("dw",), w=BASE, dw=BASE))
+    passes(ffn_backward_call(blk(save=1), want=("dx",), x=BASE, dx=BASE))
+    passes(ffn_backward_call(blk(save=1), want=("dwg", "dwu"), wg=BASE, dwg=BASE))
+    passes(ffn_backward_call(blk(save=2), x_q=BASE, dx=BASE))         # x is given
+    # every buffer that a call can have, each in a place of its own
+    passes(linear_call(lin(), res=True, with_pre=True))
+    passes(linear_backward_call(lin(fn=1)))
+    passes(ffn_call(blk(save=2)))
+    passes(ffn_backward_call(blk(save=2)))
+    passes(ffn_backward_call(blk(save=2), with_x=False))
+    # one input twice
+    passes(ffn_call(blk(), wg=BASE, wu=BASE, x=BASE))
+
+
+@NO_GPU
+def test_overlap_is_exact():
+    """Pitched rows against pitched rows, byte by byte."""
+    import random
+    rng = random.Random(5)
+    seen = set()
+    for _ in range(3000):
+        T, N, K = rng.randint(1, 5), 8 * rng.randint(1, 6), 8 * rng.randint(1, 6)
+        ldx = K + 8 * rng.randint(0, 14)
+        ldy = ldx if rng.random() < 0.4 and ldx >= N else N + 8 * rng.randint(0, 14)
+        off = 16 * rng.randint(-60, 60)
+        xs = {2 * (t * ldx + k) // 16 for t in range(T) for k in range(K)}
+        ys = {(off + 2 * (t * ldy + k)) // 16 for t in range(T) for k in range(N)}
+        want = 1 if xs & ys else 5
+        seen.add((want, ldx == ldy))
+        assert linear_call(lin(T=T, N=N, K=K, ldx=ldx, ldy=ldy), x=BASE, y=BASE + off) == want, (T, N, K, ldx, ldy, off)
+    assert len(seen) == 4

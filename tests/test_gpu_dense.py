@@ -625,3 +625,51 @@ def test_codes_of_long_sums(long_sums, T, I):
     for n, v, q, s in (("g", exact[0], saved.g, saved.g_s), ("u", exact[1], saved.u, saved.u_s)):
         assert R.check_codes(v[:T, :I], rel, q, s, n) > 0.99 * T * I
     assert (y == 0).all() and M.moe_device_status(ws) == 0
+
+
+# --- buffers that lie on or beside one another -----------------------------------------------
+
+@pytest.mark.parametrize("save", [M.SAVE_NONE, M.SAVE_16, M.SAVE_8])
+@pytest.mark.parametrize("T", [1, 9, 70, 300])
+def test_a_block_into_its_own_input(T, save):
+    """x is read before y is written: y may be x, with x as the residual or without one."""
+    H, I, dt = 520, 1032, BF
+    x, wg, wu, wd = ffn_tensors(T, H, I, dt)
+    d = M.MoeFfnDims(T=T, H=H, I=I, fn=1, save=save)
+    ws, y = workspace(M.moe_ffn_workspace_size(d)), empty((T, H), dt)
+    for residual in (False, True):
+        kept = [M.FfnSaved(d) if save else None for _ in range(2)]
+        M.moe_ffn(d, x, wg, wu, wd, x if residual else None, y, kept[0], ws)
+        inplace = x.clone()
+        M.moe_ffn(d, inplace, wg, wu, wd, inplace if residual else None, inplace, kept[1], ws)
+        assert torch.equal(inplace, y)
+        for n in ("g", "u", "g_s", "u_s", "x_q", "x_s") if save else ():
+            a, b = (getattr(k, n) for k in kept)
+            assert (a is None) == (b is None) and (a is None or torch.equal(a, b)), n
+
+
+@pytest.mark.parametrize("T", [1, 30, 300])
+def test_slices_of_one_buffer(T):
+    """x, residual and y as neighbouring columns."""
+    N, K, dt = 264, 136, BF
+    x, w, r = rand((T, K), 1, dt, 1), rand((N, K), 0.05, dt, 2), rand((T, N), 1, dt, 4)
+    ref = R.linear(x, w, None, r, "none", dt, dt)[0]
+    ld = K + 2 * N + 8
+    buf = torch.full((T, ld), 7.0, dtype=dt, device="cuda")
+    buf[:, :K], buf[:, K:K + N] = x, r
+    d = M.MoeLinearDims(T=T, N=N, K=K, ldx=ld, ldr=ld, ldy=ld)
+    M.moe_linear(d, buf[:, :K], w, None, buf[:, K:K + N], buf[:, K + N:K + 2 * N], None,
+                 workspace(M.moe_linear_workspace_size(d)))
+    R.check(buf[:, K + N:K + 2 * N], ref, "y", 1, dt)
+    assert torch.equal(buf[:, :K], x) and torch.equal(buf[:, K:K + N], r) and (buf[:, K + 2 * N:] == 7.0).all()
+
+
+def test_an_overlap_is_an_error_of_the_binding():
+    T, H, dt = 30, 264, BF
+    x, w = rand((T, H), 1, dt, 1), rand((H, H), 0.05, dt, 2)
+    d = M.MoeLinearDims(T=T, N=H, K=H)
+    kept = x.clone()
+    with pytest.raises(M.MoeError, match="y overlaps x"):
+        M.moe_linear(d, x, w, None, x, x, None, workspace(M.moe_linear_workspace_size(d)))
+    torch.cuda.synchronize()
+    assert torch.equal(x, kept)
