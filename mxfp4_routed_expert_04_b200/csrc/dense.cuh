@@ -278,5 +278,12 @@ MOE_DEV bool wait_bounded(uint64_t* bar, uint32_t parity, volatile int* abort,
   return false;
 }
 
+// Before a CTA that gave up a wait may exit: its copies, `issued` stages in turn
+// over a ring of nst, have landed (bounded; one thread)
+MOE_DEV void drain_copies(uint64_t* full, int nst, long issued) {
+  for (int i = 0; i < nst && i < issued; ++i)
+    mbar_wait(&full[i], (uint32_t)((issued - 1 - i) / nst & 1), 1u << 14);
+}
+
 }  // namespace tc
 }  // namespace moe

@@ -18,8 +18,10 @@
 //
 // Roles: warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-9 run the
 // epilogue out of one accumulator buffer while the next tile fills the other.
-// Every wait is bounded; a wait that gives up raises the CTA's abort flag and
-// the status word.
+// Every wait on a barrier in shared memory is bounded; one that gives up raises
+// the CTA's abort flag and the status word, and the CTA's own copies and MMAs
+// are waited for before it exits. (Cluster barriers and the allocation of tensor
+// memory have no bound: every CTA comes to them, whether it gave up or not.)
 #include <type_traits>
 
 #include "dense.cuh"
@@ -321,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ long issued;
   volatile int* abort = &abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -402,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
     if (tc::elect_one()) {
       int s = 0;
       uint32_t ph = 0;
-      long issued = 0;
+      long n = 0;
       bool ok = true;
       for (int q = q0; q < q1 && ok; q += dq) {
         const Tile t = tile_of(q);
@@ -440,22 +443,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
             } else {
               load(sb, mb, k0, t.n0 + (int)rank * bn);
             }
-            ++issued;
+            ++n;
             if (++s == nst) { s = 0; ph ^= 1u; }
           }
         };
         by_direction<kEpi>(p, fill);
       }
+      issued = n;
       // every stage handed back: no arrival of the pair's MMAs is left to come
       for (int i = 0; i < nst && ok; ++i) {
         ok = tc::wait_bounded(&empty[s], ph ^ 1u, abort);
         if (++s == nst) { s = 0; ph ^= 1u; }
-      }
-      if (!ok && rank == 0) {           // let every issued copy land before the CTA can exit
-        for (int i = 0; i < nst && i < issued; ++i) {
-          const long last = (issued - 1 - i) / nst;           // last use of stage i
-          mbar_wait(&full[i], (uint32_t)(last & 1), 1u << 14);
-        }
       }
     }
     __syncwarp();
@@ -498,12 +496,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
         };
         by_direction<kEpi>(p, issue);
       }
-      if (*abort) {                     // no MMA may run past the CTA's exit
-        tc::commit_cg<kCg>(&drain);
-        mbar_wait(&drain, 0);
-      }
+      tc::commit_cg<kCg>(&drain);
     }
     __syncwarp();
+    // no MMA runs past the CTA's exit, also when a wait gave up (the pair's second
+    // CTA looks when its epilogue is through, not all the while)
+    if (rank == 0) mbar_wait(&drain, 0);
   } else {
     // ---------------- epilogue (warps 2-9) ----------------
     // two warps share a quarter's 32 rows: 32-column chunks in turn
@@ -596,7 +594,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_dense_gemm(const __grid_constan
 
   tc::fence_before_sync();
   __syncthreads();
-  if (threadIdx.x == 0 && *abort) atomicOr(a.status, kStatusWaitTimeout);
+  if (threadIdx.x == 0 && *abort) {
+    atomicOr(a.status, kStatusWaitTimeout);
+    // the second CTA's copies count on the first one's barriers: it gives its own
+    // time to land by a barrier that nothing completes
+    if (rank == 0) tc::drain_copies(full, nst, issued);
+    else mbar_wait(&full[0], 0, 1u << 8);
+  }
+  if (rank != 0 && warp == 1) mbar_wait(&drain, 0);
+  __syncwarp();
   if (kCg > 1) tc::cluster_sync();      // the pair's MMAs read both CTAs' memory
   if (warp == 1) {
     tc::fence_after_sync();
@@ -670,9 +676,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t full[kSplitStages], empty[kSplitStages], acc_full;
+  __shared__ uint64_t full[kSplitStages], empty[kSplitStages], acc_full, drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, issued;
   volatile int* abort = &abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tn = a.tile_n, cols = kEpi == kEpiGlu ? tn / 2 : tn;
@@ -695,6 +701,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
       mbar_init(&empty[s], 1);
     }
     mbar_init(&acc_full, 1);
+    mbar_init(&drain, 1);
     abort_flag = 0;
     fence_mbar_init();
     tc::prefetch_map(&p.map_a[p.m_segs > 1 ? seg : 0]);
@@ -711,12 +718,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (tc::elect_one()) {
-      int s = 0, issued = 0;
+      int s = 0, n = 0;
       uint32_t ph = 0;
-      bool ok = true;
       auto fill = [&](auto a_mn, auto b_mn) {
         for (int j = j0; j < j1; ++j) {
-          if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
+          if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) break;
           uint8_t* sa = smem + s * stage_bytes;
           uint8_t* sb = sa + kATile;
           const int kseg = j >= ks1 ? 1 : 0, k0 = (j - kseg * ks1) * 64;
@@ -737,14 +743,12 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
           } else {
             tc::tma_load_2d(sb, mb, k0, n0, &full[s]);
           }
-          ++issued;
+          ++n;
           if (++s == nst) { s = 0; ph ^= 1u; }
         }
       };
       by_direction<kEpi>(p, fill);
-      if (!ok) {                        // let every issued copy land before the CTA can exit
-        for (int i = 0; i < nst && i < issued; ++i) mbar_wait(&full[i], (uint32_t)((issued - 1 - i) / nst & 1), 1u << 14);
-      }
+      issued = n;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -768,9 +772,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
         }
       };
       by_direction<kEpi>(p, issue);
-      tc::commit_cg<1>(&acc_full);      // also when it gave up: no MMA may run past the CTA's exit
+      tc::commit_cg<1>(&acc_full);
+      tc::commit_cg<1>(&drain);
     }
     __syncwarp();
+    mbar_wait(&drain, 0);               // no MMA runs past the CTA's exit, also when a wait gave up
   } else {
     // ---------------- this CTA's sums, over the ring (warps 2-5) ----------------
     const int wq = warp & 3;
@@ -816,7 +822,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0 && *abort) atomicOr(a.status, kStatusWaitTimeout);
+  if (threadIdx.x == 0 && *abort) {
+    atomicOr(a.status, kStatusWaitTimeout);
+    tc::drain_copies(full, nst, issued);
+  }
+  __syncwarp();
   if (splits > 1) tc::cluster_sync();   // the other CTAs read this one's sums
   if (warp == 1) {
     tc::fence_after_sync();

@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  __shared__ uint64_t full[kDenseRowsStages], empty[kDenseRowsStages], acc_full[2], acc_empty[2];
+  __shared__ uint64_t full[kDenseRowsStages], empty[kDenseRowsStages], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
+  __shared__ int abort_flag, issued;
   volatile int* abort = &abort_flag;
   constexpr int kRows = kEpi == kEpiGlu ? 64 : 128;         // outputs of a tile
   constexpr int kPer = kRows / 32;                          // units of 4 tokens
@@ -232,6 +232,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
     }
+    mbar_init(&drain, 1);
     abort_flag = 0;
     fence_mbar_init();
   }
@@ -274,16 +275,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       for (int i = 0; i < pre; ++i) load_x(i, j0 + i);
       int s = pre == nst ? 0 : pre;
       uint32_t ph = pre == nst ? 1u : 0u;
-      bool ok = true;
-      for (int j = j0 + pre; j < j1; ++j) {
-        if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) { ok = false; break; }
+      int j = j0 + pre;
+      for (; j < j1; ++j) {
+        if (!tc::wait_bounded(&empty[s], ph ^ 1u, abort)) break;
         load_w(s, j);
         load_x(s, j);
         if (++s == nst) { s = 0; ph ^= 1u; }
       }
-      if (!ok) {                        // let every issued copy land before the CTA can exit
-        for (int i = 0; i < nst; ++i) mbar_wait(&full[i], i < s ? ph : ph ^ 1u, 1u << 14);
-      }
+      issued = j - j0;
     }
     __syncwarp();
     pdl_wait();
@@ -314,8 +313,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
           tc::commit_cg<1>(&empty[s]);
           if (++s == nst) { s = 0; ph ^= 1u; }
         }
-        tc::commit_cg<1>(&acc_full[buf]);       // also when it gave up: no MMA may run past the CTA's exit
+        tc::commit_cg<1>(&acc_full[buf]);
       }
+      tc::commit_cg<1>(&drain);
     }
     __syncwarp();
   } else {
@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
       }
     }
   }
+  if (warp == 1) mbar_wait(&drain, 0);  // no MMA runs past the CTA's exit, also when a wait gave up
   __syncwarp();
   tc::fence_before_sync();
   cluster_arrive();
@@ -460,7 +461,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) k_dense_rows(const __grid_con
     if (kEpi == kEpiLinear) inputs(u + step, bias, res);
   }
   __syncthreads();
-  if (threadIdx.x == 0 && *abort) atomicOr(a.status, kStatusWaitTimeout);
+  if (threadIdx.x == 0 && *abort) {
+    atomicOr(a.status, kStatusWaitTimeout);
+    tc::drain_copies(full, nst, issued);
+  }
+  __syncwarp();
   if (!push) {                          // the other CTAs fetch this one's sums
     cluster_arrive();
     cluster_wait();
