@@ -354,12 +354,14 @@ moe_status moe_latent_down(const moe_dims* dims, const uint16_t* x, const uint16
  * every role of the CTA stops, and bit 2 (value 4) of the status word is set
  * (see moe_device_status). This call runs one CTA that uses the same waits
  * on one 512-byte stage, with `limit` tries (1..4096; about 20 us each at
- * most) instead of the multi-second default:
+ * most) instead of the multi-second default (waits that go by the clock:
+ * `limit` microseconds, looked at every millisecond at least):
  *   deliver != 0: the stage is filled by a bulk copy from `src` (a 16-byte
  *     aligned DEVICE buffer of 512 bytes); the waits succeed and *status is
  *     left unchanged;
- *   deliver == 0: nothing delivers the stage's bytes; both waits give up, the
+ *   deliver == 0: nothing delivers the stage's bytes; all waits give up, the
  *     kernel returns and ORs 4 into *status (a DEVICE int32).
+ * Waits that do not agree with each other set bit 16.
  * No copy is in flight when a wait gives up, so the context stays usable.
  * Enqueued on `stream`; invalid arguments return an error and enqueue nothing.
  */

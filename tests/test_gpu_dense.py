@@ -627,6 +627,26 @@ def test_codes_of_long_sums(long_sums, T, I):
     assert (y == 0).all() and M.moe_device_status(ws) == 0
 
 
+# --- waits that run out ---------------------------------------------------------------------
+
+def test_waits_of_the_dense_kernels_run_out():
+    """By the clock, through another role's flag, and all alike: bit 2 of the
+    status word, long before the seconds that the follower was given."""
+    status = torch.zeros(2, dtype=torch.int32, device="cuda")
+    src = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    M.moe_selftest_bounded_wait(status, src, True, 4096)
+    torch.cuda.synchronize()
+    assert int(status[0]) == 0
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    M.moe_selftest_bounded_wait(status, None, False, 100)
+    end.record()
+    torch.cuda.synchronize()
+    assert int(status[0]) == M.STATUS_WAIT_TIMEOUT
+    assert start.elapsed_time(end) < 1000      # ms; the follower's own limit is 4 s
+    assert int(status[1]) == 0
+
+
 # --- buffers that lie on or beside one another -----------------------------------------------
 
 @pytest.mark.parametrize("save", [M.SAVE_NONE, M.SAVE_16, M.SAVE_8])
