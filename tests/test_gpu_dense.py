@@ -627,6 +627,84 @@ def test_codes_of_long_sums(long_sums, T, I):
     assert (y == 0).all() and M.moe_device_status(ws) == 0
 
 
+# --- activations over their whole range --------------------------------------------------
+
+def arguments(dt):
+    """512 arguments of an activation: a grid over [-13, 13], ever larger ones, both zeros."""
+    z = torch.linspace(-13, 13, 470, dtype=torch.float64)
+    far = torch.tensor([0.0, 1e-7, 14.0, 17.0, 20.0, 40.0, 60.0, 80.0, 86.0, 87.0, 87.5, 88.0, 88.5, 89.0, 104.0, 300.0,
+                        1e3, 1e4, 3e4, 6e4, torch.finfo(dt).max], dtype=torch.float64)
+    return torch.cat([z, far, -far]).to(dt)
+
+
+def exp_unit(a):
+    """Relative bound of __expf at a, as the CUDA programming guide states it, and of a's own rounding."""
+    return (2 + 1.173 * a.abs()) * 2.0 ** -23 + a.abs() * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T", [1, 16, 80])
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("fn", ["silu", "gelu", "relu"])
+def test_activation_values_over_their_range(fn, dt, T):
+    """In fp32, through a projection by the identity (its sums are exact).
+    silu: the exponential, 1 + e, the quotient (2 units; 0 once the divisor
+    passes 2^126) and a last rounding. gelu: the exponential, a quotient, the
+    fitted polynomial (5.5e-7) and three products of the tail; above 0 the
+    complement rounds once more."""
+    z = arguments(dt)[:512].cuda()
+    n = z.numel()
+    x = z.expand(T, n).contiguous()
+    d = M.MoeLinearDims(T=T, N=n, K=n, fn=R.FN[fn], dtype=code(dt), out_f32=1)
+    y = empty((T, n), F32)
+    M.moe_linear(d, x, torch.eye(n, dtype=dt, device="cuda"), None, None, y, None,
+                 workspace(M.moe_linear_workspace_size(d)))
+    v = z.double()
+    f = R.value(fn, v)
+    if fn == "silu":
+        e = f.abs() * (exp_unit(v.clamp(-104, 104)) + 6 * 2.0 ** -24) + 89 * 2.0 ** -126
+    elif fn == "gelu":
+        rel = exp_unit(v.clamp(-14, 14) ** 2 / 2) + 5.5e-7 + 8 * 2.0 ** -24
+        tail = v.abs() * 0.5 * torch.special.erfc(v.abs() / 2 ** 0.5)
+        e = tail * rel + torch.where(v > 0, f * 2.0 ** -23, 0) + 2.0 ** -126
+    else:
+        e = torch.zeros_like(f)
+    for t in (0, T - 1):
+        R.check(y[t], (f, e), fn)
+
+
+@pytest.mark.parametrize("dt", [BF, HF])
+@pytest.mark.parametrize("fn", ["silu", "gelu", "relu"])
+def test_activation_slopes_over_their_range(fn, dt):
+    """In fp32, as the bias gradient of one token with dy = 1. silu, p (1 + z (1 - p)):
+    p is off by its quotient's units, 1 - p by p's error and a rounding of p's
+    size, which z magnifies. gelu, Phi + z phi: the errors of both terms."""
+    z = arguments(dt)[:512].cuda().reshape(1, -1)
+    n = z.numel()
+    d = M.MoeLinearDims(T=1, N=n, K=8, fn=R.FN[fn], dtype=code(dt), out_f32=1)
+    db = empty((n,), F32)
+    M.moe_linear_backward(d, torch.ones_like(z), None, None, z, None, None, db,
+                          workspace(M.moe_linear_workspace_size(d)))
+    v = z.double().reshape(-1)
+    s = R.slope(fn, v)
+    if fn == "silu":
+        p, q = torch.sigmoid(v), torch.sigmoid(-v)
+        ep = p * (q * exp_unit(v.clamp(-104, 104)) + 6 * 2.0 ** -24) + 2.0 ** -126
+        one = (1 + v * q).abs()
+        # 1 - p is exact once p has rounded to 1: then q itself, below 2^-24, is what is lost
+        inner = v.abs() * torch.minimum(ep + 2.0 ** -24, q + 2.0 ** -22) + 3 * 2.0 ** -24 * (1 + v.abs() * q)
+        e = ep * (one + inner) + p * inner + 2.0 ** -23 * s.abs()
+        e = torch.where(v > 60, torch.full_like(e, 2.0 ** -20), e)      # p is 1, the slope 1
+    elif fn == "gelu":
+        a = v.clamp(-14, 14) ** 2 / 2
+        phi = v.abs() * torch.exp(-v * v / 2) / (2 * torch.pi) ** 0.5
+        tail = 0.5 * torch.special.erfc(v.abs() / 2 ** 0.5)
+        e = phi * (exp_unit(a) + 3 * 2.0 ** -24) + tail * (exp_unit(a) + 5.5e-7 + 8 * 2.0 ** -24) \
+            + torch.where(v > 0, 2.0 ** -23, 0.0) + 2.0 ** -23 * s.abs() + 2.0 ** -126
+    else:
+        e = torch.zeros_like(s)
+    R.check(db, (s, e), fn)
+
+
 # --- waits that run out ---------------------------------------------------------------------
 
 def test_waits_of_the_dense_kernels_run_out():
