@@ -771,3 +771,133 @@ def test_an_overlap_is_an_error_of_the_binding():
         M.moe_linear(d, x, w, None, x, x, None, workspace(M.moe_linear_workspace_size(d)))
     torch.cuda.synchronize()
     assert torch.equal(x, kept)
+
+
+# --- order of calls ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("save", [M.SAVE_NONE, M.SAVE_8])
+@pytest.mark.parametrize("T", [1, 8, 9, 40, 64, 200])
+def test_weights_written_by_the_calls_before_a_block(T, save):
+    """wg, wu and wd, each a projection's output, wd the last one before the
+    block: other weights every time, so that early reads of them show."""
+    H, I, K, dt = 1032, 2056, 1000, BF
+    x = rand((T, H), 1, dt, 1)
+    dims = [M.MoeLinearDims(T=n, N=k, K=K) for n, k in ((I, H), (I, H), (H, I))]
+    ws = workspace(max(M.moe_linear_workspace_size(d) for d in dims))
+    d = M.MoeFfnDims(T=T, H=H, I=I, fn=1, save=save)
+    wsf = workspace(M.moe_ffn_workspace_size(d))
+    w = [empty((e.T, e.N), dt) for e in dims]
+    y = empty((T, H), dt)
+    saved = M.FfnSaved(d) if save else None
+    parts = [[(rand((e.T, K), 0.2, dt, 10 * i + j), rand((e.N, K), 0.2 / K ** 0.5, dt, 100 + 10 * i + j))
+              for j, e in enumerate(dims)] for i in range(4)]
+    outs = []
+    for _ in range(2):
+        for p in parts:
+            for e, (a, b), out in zip(dims, p, w):
+                M.moe_linear(e, a, b, None, None, out, None, ws)
+            M.moe_ffn(d, x, *w, None, y, saved, wsf)
+            outs.append(y.clone())
+    # the same in a graph
+    held = [torch.empty_like(y) for _ in parts]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for p, h in zip(parts, held):
+            for e, (a, b), out in zip(dims, p, w):
+                M.moe_linear(e, a, b, None, None, out, None, ws)
+            M.moe_ffn(d, x, *w, None, y, saved, wsf)
+            h.copy_(y)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(h, o) for h, o in zip(held, outs))
+    del graph
+    for i, p in enumerate(parts):
+        exact = [R.linear(a, b, None, None, "none", dt, dt)[0][0].to(dt) for a, b in p]
+        for e, (a, b), out in zip(dims, p, w):
+            M.moe_linear(e, a, b, None, None, out, None, ws)
+            torch.cuda.synchronize()
+        assert all(((o.double() - v.double()).norm() <= 2 * R.unit(dt) * v.double().norm()) for o, v in zip(w, exact))
+        ref = R.ffn(x, *w, None, "silu", dt, dt)[0]
+        for o in (outs[i], outs[i + len(parts)]):
+            R.check(o, ref, "y", 2, dt)
+
+
+def test_two_streams_give_what_one_gives():
+    """Forward and backward on two streams at once: the bits of the same calls made alone."""
+    H, I, dt = 520, 1032, BF
+    for T in (1, 9, 30, 100, 400):
+        x, wg, wu, wd = ffn_tensors(T, H, I, dt)
+        dy = rand((T, H), 0.3, dt, 6)
+        d = M.MoeFfnDims(T=T, H=H, I=I, fn=1, save=M.SAVE_16)
+
+        def buffers():
+            return M.FfnSaved(d), empty((T, H), dt), ffn_buffers(T, H, I, dt), workspace(M.moe_ffn_workspace_size(d))
+
+        def step(saved, y, got, ws, stream=None):
+            M.moe_ffn(d, x, wg, wu, wd, None, y, saved, ws, stream=stream)
+            M.moe_ffn_backward(d, dy, x, wg, wu, wd, saved, got["dx"], got["dwg"], got["dwu"], got["dwd"], ws,
+                               stream=stream)
+
+        alone = buffers()
+        step(*alone)
+        torch.cuda.synchronize()
+        runs = [(torch.cuda.Stream(), buffers()) for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for s, b in runs:
+                step(*b, stream=s)
+        torch.cuda.synchronize()
+        for _, b in runs:
+            assert torch.equal(b[1], alone[1])
+            for n in alone[2]:
+                assert torch.equal(b[2][n], alone[2][n]), n
+
+
+# --- offsets past 32 bits in the gated block and the backward passes ---------------------------
+
+def test_linear_gradient_offsets_past_32_bits():
+    """65536 x 65536 output gradients: dx by rows, dw and db by columns."""
+    T = N = 65536
+    K, dt = 16, BF
+    x, w, dy, pre = rand((T, K), 1, dt, 1), rand((N, K), 0.3, dt, 2), rand((T, N), 0.01, dt, 3), rand((T, N), 1.5, dt, 4)
+    d = M.MoeLinearDims(T=T, N=N, K=K, fn=1)
+    dx, dw, db = empty((T, K), dt), empty((N, K), dt), empty((N,), dt)
+    M.moe_linear_backward(d, dy, x, w, pre, dx, dw, db, workspace(M.moe_linear_workspace_size(d)))
+    for r0 in (0, 32760, 65500):
+        part = slice(r0, r0 + 36)
+        ref = R.linear_grads(dy[part], x[part], w, pre[part], "silu", False, dt, dt)
+        R.check(dx[part], ref["dx"], "dx")
+        ref = R.linear_grads(dy[:, part], x, w[part], pre[:, part], "silu", True, dt, dt)
+        R.check(dw[part], ref["dw"], "dw")
+        R.check(db[part], ref["db"], "db")
+
+
+@pytest.mark.parametrize("save", [M.SAVE_16, M.SAVE_8])
+def test_ffn_offsets_past_32_bits(save):
+    """65536 tokens of 65536 hidden elements, forward and backward."""
+    T = I = 65536
+    H, dt = 16, BF
+    x, wg, wu, wd = (rand((T, H), 1, dt, 1), rand((I, H), 0.3, dt, 2), rand((I, H), 0.3, dt, 3),
+                     rand((H, I), 0.01, dt, 4))
+    dy = rand((T, H), 0.3, dt, 6)
+    d = M.MoeFfnDims(T=T, H=H, I=I, fn=1, save=save)
+    ws, saved = workspace(M.moe_ffn_workspace_size(d)), M.FfnSaved(d)
+    y, got = empty((T, H), dt), ffn_buffers(T, H, I, dt)
+    M.moe_ffn(d, x, wg, wu, wd, None, y, saved, ws)
+    M.moe_ffn_backward(d, dy, x, wg, wu, wd, saved, got["dx"], got["dwg"], got["dwu"], got["dwd"], ws)
+    for r0 in (0, 32768, 65504):
+        part = slice(r0, r0 + 32)
+        R.check(y[part], R.ffn(x[part], wg, wu, wd, None, "silu", dt, dt)[0], "y")
+        g, u = saved.g[part], saved.u[part]
+        gc, uc = saved.g[:, part], saved.u[:, part]
+        if save == M.SAVE_8:
+            block = slice(r0 // 32, r0 // 32 + 1)
+            g, u = R.unpack8(g, saved.g_s[part]), R.unpack8(u, saved.u_s[part])
+            gc, uc = R.unpack8(gc, saved.g_s[:, block]), R.unpack8(uc, saved.u_s[:, block])
+        ref = R.ffn_grads(dy[part], x[part], wg, wu, wd, g, u, "silu", dt, dt)
+        R.check(got["dx"][part], ref["dx"], "dx")
+        ref = R.ffn_grads(dy, x, wg[part], wu[part], wd[:, part], gc, uc, "silu", dt, dt)
+        R.check(got["dwg"][part], ref["dwg"], "dwg")
+        R.check(got["dwu"][part], ref["dwu"], "dwu")
+        R.check(got["dwd"][:, part], ref["dwd"], "dwd")
