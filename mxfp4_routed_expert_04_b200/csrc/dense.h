@@ -72,7 +72,7 @@ constexpr int pieces_of(int stages) { return (stages + kPieceStages - 1) / kPiec
 
 template <int kEpi, int kCg, bool kPieces>
 __global__ void k_dense_gemm(const __grid_constant__ DenseGemmArgs a);
-// small products: one tile of 128 rows and 64 or 128 columns per cluster of `splits` CTAs
+// one small product: a tile of 128 rows and 64 or 128 columns per cluster of `splits` (2 to 8) CTAs
 template <int kEpi>
 __global__ void k_dense_split(const __grid_constant__ DenseGemmArgs a, int splits, int stages);
 constexpr int kMaxSplits = 8, kSplitStages = 8;

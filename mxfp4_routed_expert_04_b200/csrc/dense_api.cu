@@ -252,7 +252,7 @@ cudaError_t allow_rows() {
 }
 template <typename K>
 cudaError_t resident(K kernel, int threads, size_t smem, int (&out)[moe::kMaxSplits + 1]) {
-  for (int s = 1; s <= moe::kMaxSplits; ++s) {
+  for (int s = 2; s <= moe::kMaxSplits; ++s) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = s;

@@ -686,12 +686,10 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
   const int rank = (int)blockIdx.x % splits, q = (int)blockIdx.x / splits;
 
   // the tile: column tiles of a row tile follow each other
-  int pi = 0;
-  while (pi + 1 < a.problems && q >= a.p[pi + 1].first) ++pi;
-  const DenseProblem& p = a.p[pi];
+  const DenseProblem& p = a.p[0];
   const int mt1 = (p.M + 127) / 128, nt = (p.N + cols - 1) / cols;
-  const int m = (q - p.first) / nt, seg = m / mt1;
-  const int m0 = (m - seg * mt1) * 128, n0 = (q - p.first - m * nt) * cols;
+  const int m = q / nt, seg = m / mt1;
+  const int m0 = (m - seg * mt1) * 128, n0 = (q - m * nt) * cols;
   const int ks1 = (p.K + 63) / 64, ks = ks1 * p.k_segs;
   const int j0 = (int)((long)ks * rank / splits), j1 = (int)((long)ks * (rank + 1) / splits);
 
@@ -796,8 +794,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
     __syncwarp();
   }
   tc::fence_before_sync();
-  if (splits > 1) tc::cluster_sync();
-  else __syncthreads();
+  tc::cluster_sync();
   if (warp >= 2) {
     // ---------------- the tile's 32 x 32 blocks, dealt to the cluster's warps ----------------
     const uint32_t stage = smem_u32(smem + 128 * tn * 4) + 4096u * (uint32_t)(warp - 2);
@@ -827,7 +824,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) k_dense_split(const __grid_c
     tc::drain_copies(full, nst, issued);
   }
   __syncwarp();
-  if (splits > 1) tc::cluster_sync();   // the other CTAs read this one's sums
+  tc::cluster_sync();                   // the other CTAs read this one's sums
   if (warp == 1) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tbase, tn <= 64 ? 64u : 128u);
